@@ -7,12 +7,20 @@ library is missing or a tensor is not on a CUDA device, the call raises.
     import gated_deltanet_layer_02_b200 as gdn
     out, SN, convN = gdn.chunk_prefill(x, beta, g, cu_seqlens, conv_w=w, z=z, norm_w=nw)
     out = gdn.decode_step(x_t, beta_t, g_t, conv_state, S, conv_w=w, z=z_t, norm_w=nw)
+
+The selective state space layer over the same packed sequences and state pools, and the index
+tables of a serving step:
+
+    y, SN, convN = gdn.ssm_prefill(x, dt, a_log, cu_seqlens, w, D=D, z=z, dims=gdn.SsmDims())
+    y = gdn.ssm_decode_step(x_t, dt_t, a_log, conv_state, S, w, D=D, z=z_t, slot_idx=slot)
+    t = gdn.batch_tables(ctx_lens, new_lens, slot, page_table, free_pages, free_head, 64, rows)
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+import typing
 
 import torch
 
@@ -20,7 +28,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
 
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_TIMEOUT, \
-    GDN_ERR_WORKSPACE, GDN_ERR_BOUNDS = 0, -1, -2, -3, -4, -5, -6
+    GDN_ERR_WORKSPACE, GDN_ERR_BOUNDS, GDN_ERR_PAGES = 0, -1, -2, -3, -4, -5, -6, -7
 GDN_F32, GDN_BF16 = 0, 1
 
 #: every symbol include/gdn.h declares
@@ -33,7 +41,9 @@ EXPORTS = (
     "gdn_chunk_prefill_states", "gdn_decode_multi", "gdn_block_prefill_workspace_size",
     "gdn_block_prefill", "gdn_chunk_prefill_slots", "gdn_chunk_prefill_host_plan",
     "gdn_chunk_prefill_host_workspace_size", "gdn_chunk_prefill_host", "gdn_debug_set",
-    "gdn_chunk_prefill_pages",
+    "gdn_chunk_prefill_pages", "gdn_ssm_conv_channels", "gdn_ssm_prefill_workspace_size",
+    "gdn_ssm_prefill", "gdn_ssm_prefill_slots", "gdn_ssm_decode_workspace_size",
+    "gdn_ssm_decode_step", "gdn_batch_tables",
 )
 
 #: size of the library-owned scratch used by chunk_prefill_static_ws (GDN_STATIC_WORKSPACE_BYTES)
@@ -70,6 +80,23 @@ class Dims(ctypes.Structure):
     @property
     def channels(self) -> int:
         return (2 * self.num_k_heads + self.num_v_heads) * self.head_dim
+
+
+class SsmDims(ctypes.Structure):
+    """gdn_ssm_dims: shape of a selective state space layer (H heads of head_dim channels, G
+    groups of heads that share B and C, state_dim columns of the state)."""
+    _fields_ = [("num_heads", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("state_dim", ctypes.c_int32),
+                ("conv_kernel", ctypes.c_int32), ("dt_min", ctypes.c_float),
+                ("dt_max", ctypes.c_float)]
+
+    def __init__(self, num_heads=64, num_groups=8, head_dim=64, state_dim=128, conv_kernel=4,
+                 dt_min=0.0, dt_max=float("inf")):
+        super().__init__(num_heads, num_groups, head_dim, state_dim, conv_kernel, dt_min, dt_max)
+
+    @property
+    def channels(self) -> int:
+        return self.num_heads * self.head_dim + 2 * self.num_groups * self.state_dim
 
 
 _lib = None
@@ -129,6 +156,21 @@ def _configure(L):
     L.gdn_debug_set.argtypes = [ctypes.POINTER(DebugOptions)]
     L.gdn_chunk_prefill_static_ws.argtypes = [dp, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp,
                                               i32, i32, vp, vp, vp, vp, vp, vp, vp]
+    sp = ctypes.POINTER(SsmDims)
+    L.gdn_ssm_conv_channels.argtypes = [sp]
+    L.gdn_ssm_conv_channels.restype = ctypes.c_int64
+    L.gdn_ssm_prefill_workspace_size.argtypes = [sp, ctypes.c_int, i32, i32]
+    L.gdn_ssm_prefill_workspace_size.restype = ctypes.c_size_t
+    L.gdn_ssm_prefill.argtypes = [sp, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32,
+                                  vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
+    L.gdn_ssm_prefill_slots.argtypes = [sp, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32,
+                                        i32, vp, i32, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
+    L.gdn_ssm_decode_workspace_size.argtypes = [sp, i32]
+    L.gdn_ssm_decode_workspace_size.restype = ctypes.c_size_t
+    L.gdn_ssm_decode_step.argtypes = [sp, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp,
+                                      vp, vp, vp, vp, i32, i32, vp, vp, ctypes.c_size_t, vp, vp]
+    L.gdn_batch_tables.argtypes = [vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, i32, i32, vp, vp,
+                                   vp, vp, vp, vp]
     for name in EXPORTS:  # every declared symbol must resolve
         getattr(L, name)
     return L
@@ -533,6 +575,228 @@ def block_prefill(h, w_qkv, w_z, w_ba, a_log, dt_bias, w_out, cu_seqlens, conv_w
     return y, SN, convN
 
 
+def _arg(t, name, dtype, n, dev, required=False):
+    """Address of a contiguous CUDA tensor of at least n elements on device `dev` (None: absent)."""
+    if t is None:
+        if required:
+            raise ValueError(f"{name} is required")
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements; the call needs {n}")
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must live on a CUDA device (no CPU fallback)")
+        raise ValueError(f"{name} is on {t.device}; the call runs on cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _call_on(dev, name, *args):
+    """One library call with device `dev` current, on that device's current stream."""
+    fn = getattr(lib(), name)
+    if dev == torch.cuda.current_device():
+        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _check(name, code)
+
+
+def ssm_conv_channels(dims: SsmDims) -> int:
+    return int(lib().gdn_ssm_conv_channels(ctypes.byref(dims)))
+
+
+def ssm_prefill_workspace_size(num_seqs: int, num_tokens: int, dtype=torch.bfloat16,
+                               dims: SsmDims | None = None) -> int:
+    return int(lib().gdn_ssm_prefill_workspace_size(
+        ctypes.byref(dims or SsmDims()), GDN_BF16 if dtype == torch.bfloat16 else GDN_F32,
+        num_seqs, num_tokens))
+
+
+def _cuda_index(t, name):
+    """Device of the call: that of its first tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t.get_device()
+
+
+def _ssm_weights(dims, dt_x, dev, conv_w, conv_b, dt, dt_bias, a_log, D, T):
+    Cc, H = dims.channels, dims.num_heads
+    return (_arg(conv_w, "conv_w", dt_x, Cc * dims.conv_kernel, dev, True),
+            _arg(conv_b, "conv_b", dt_x, Cc, dev),
+            _arg(dt, "dt", torch.float32, T * H, dev, True),
+            _arg(dt_bias, "dt_bias", torch.float32, H, dev),
+            _arg(a_log, "a_log", torch.float32, H, dev, True),
+            _arg(D, "D", torch.float32, H, dev))
+
+
+def ssm_prefill(x, dt, a_log, cu_seqlens, conv_w, conv_b=None, dt_bias=None, D=None, z=None,
+                S0=None, SN=None, conv0=None, convN=None, out=None, workspace=None,
+                dev_status=None, want_state=True, dims: SsmDims | None = None):
+    """The selective state space layer over packed sequences.  Returns (out, SN, convN).
+
+    x [T, Cc] rows [x | B | C], dt [T, H] fp32 (before dt_bias and the softplus), a_log, dt_bias,
+    D [H] fp32, conv_w [Cc, 4], conv_b [Cc], z [T, H, P] or None, cu_seqlens [N+1] int32 (device),
+    S0 [N, H, P, state_dim] fp32 or None, conv0 [N, 3, Cc] or None.  Rows of out behind the last
+    sequence (cu_seqlens[N] < T) are left as they were."""
+    dims = dims or SsmDims()
+    code, dtx, T, N = _act_dtype(x), x.dtype, x.shape[0], cu_seqlens.numel() - 1
+    H, P, Ns, Cc = dims.num_heads, dims.head_dim, dims.state_dim, dims.channels
+    dev = _cuda_index(x, "x")
+    px = _arg(x, "x", dtx, T * Cc, dev)
+    w = _ssm_weights(dims, dtx, dev, conv_w, conv_b, dt, dt_bias, a_log, D, T)
+    pz = _arg(z, "z", dtx, T * H * P, dev)
+    pcu = _arg(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev)
+    if not x.is_cuda:
+        raise ValueError("x must live on a CUDA device (no CPU fallback)")
+    if out is None:
+        out = torch.empty((T, H, P), dtype=dtx, device=x.device)
+    if want_state and SN is None:
+        SN = torch.empty((N, H, P, Ns), dtype=torch.float32, device=x.device)
+    if want_state and convN is None:
+        convN = torch.empty((N, dims.conv_kernel - 1, Cc), dtype=dtx, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(ssm_prefill_workspace_size(N, T, dtx, dims), dtype=torch.uint8,
+                                device=x.device)
+    n_s, n_c = N * H * P * Ns, N * (dims.conv_kernel - 1) * Cc
+    _call_on(dev, "gdn_ssm_prefill", ctypes.byref(dims), code, px, *w, pz, pcu, N, T,
+             _arg(S0, "S0", torch.float32, n_s, dev), _arg(SN, "SN", torch.float32, n_s, dev),
+             _arg(conv0, "conv0", dtx, n_c, dev), _arg(convN, "convN", dtx, n_c, dev),
+             _arg(out, "out", dtx, T * H * P, dev),
+             _arg(workspace, "workspace", torch.uint8, 0, dev), workspace.numel(),
+             _arg(dev_status, "dev_status", torch.int32, 1, dev))
+    return out, SN, convN
+
+
+def ssm_prefill_slots(x, dt, a_log, cu_seqlens, S_pool, conv_w, slot_idx=None, conv_pool=None,
+                      conv_b=None, dt_bias=None, D=None, z=None, out=None, workspace=None,
+                      dev_status=None, dims: SsmDims | None = None):
+    """ssm_prefill with the states in pools shared with ssm_decode_step: sequence n starts from and
+    overwrites S_pool[slot_idx[n]] ([slots, H, P, state_dim] fp32) and conv_pool[slot_idx[n]]
+    ([slots, 3, Cc]).  Slots as in chunk_prefill_slots.  Returns out [T, H, P]."""
+    dims = dims or SsmDims()
+    code, dtx, T, N = _act_dtype(x), x.dtype, x.shape[0], cu_seqlens.numel() - 1
+    H, P = dims.num_heads, dims.head_dim
+    dev = _cuda_index(x, "x")
+    px = _arg(x, "x", dtx, T * dims.channels, dev)
+    w = _ssm_weights(dims, dtx, dev, conv_w, conv_b, dt, dt_bias, a_log, D, T)
+    pz = _arg(z, "z", dtx, T * H * P, dev)
+    pcu = _arg(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev)
+    rows = _ssm_pool_rows(S_pool, conv_pool, dims)
+    if slot_idx is None and rows < N:
+        raise ValueError(f"the pools hold {rows} rows; the call needs {N}")
+    pslot = _arg(slot_idx, "slot_idx", torch.int32, N, dev)
+    pS = _arg(S_pool, "S_pool", torch.float32, 0, dev, True)
+    pc = _arg(conv_pool, "conv_pool", dtx, 0, dev)
+    if not x.is_cuda:
+        raise ValueError("x must live on a CUDA device (no CPU fallback)")
+    if out is None:
+        out = torch.empty((T, H, P), dtype=dtx, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(ssm_prefill_workspace_size(N, T, dtx, dims), dtype=torch.uint8,
+                                device=x.device)
+    _call_on(dev, "gdn_ssm_prefill_slots", ctypes.byref(dims), code, px, *w, pz, pcu, N, T, pslot,
+             rows, pS, pc, _arg(out, "out", dtx, T * H * P, dev),
+             _arg(workspace, "workspace", torch.uint8, 0, dev), workspace.numel(),
+             _arg(dev_status, "dev_status", torch.int32, 1, dev))
+    return out
+
+
+def _ssm_pool_rows(S, conv_state, dims):
+    """Rows of a state pool pair: whole states in S that have a conv history row."""
+    rows = S.numel() // (dims.num_heads * dims.head_dim * dims.state_dim) if S is not None else 0
+    if conv_state is not None:
+        rows = min(rows, conv_state.numel() // ((dims.conv_kernel - 1) * dims.channels))
+    return rows
+
+
+def ssm_decode_step(x, dt, a_log, conv_state, S, conv_w, conv_b=None, dt_bias=None, D=None, z=None,
+                    slot_idx=None, out=None, workspace=None, dev_status=None,
+                    dims: SsmDims | None = None):
+    """One token per sequence; conv_state [slots, 3, Cc] and S [slots, H, P, state_dim] (fp32 or
+    bf16) are updated in place.  Returns out [B, H, P].  A slot outside the pools is skipped on the
+    device and reported in dev_status (GDN_ERR_INVALID_ARG)."""
+    dims = dims or SsmDims()
+    code, dtx, B = _act_dtype(x), x.dtype, x.shape[0]
+    H, P, Cc = dims.num_heads, dims.head_dim, dims.channels
+    dev = _cuda_index(x, "x")
+    px = _arg(x, "x", dtx, B * Cc, dev)
+    w = _ssm_weights(dims, dtx, dev, conv_w, conv_b, dt, dt_bias, a_log, D, B)
+    pz = _arg(z, "z", dtx, B * H * P, dev)
+    rows = _ssm_pool_rows(S, conv_state, dims)
+    if slot_idx is None and rows < B:   # identity slots: rows 0 .. B-1 of the pools
+        raise ValueError(f"the state pools hold {rows} rows; the call needs {B}")
+    pslot = _arg(slot_idx, "slot_idx", torch.int32, B, dev)
+    pc = _arg(conv_state, "conv_state", dtx, 0, dev, True)
+    bf16_state = S is not None and S.dtype == torch.bfloat16
+    pS = _arg(S, "S", torch.bfloat16 if bf16_state else torch.float32, 0, dev, True)
+    if not x.is_cuda:
+        raise ValueError("x must live on a CUDA device (no CPU fallback)")
+    if out is None:
+        out = torch.empty((B, H, P), dtype=dtx, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(lib().gdn_ssm_decode_workspace_size(ctypes.byref(dims), B),
+                                dtype=torch.uint8, device=x.device)
+    _call_on(dev, "gdn_ssm_decode_step", ctypes.byref(dims), code,
+             GDN_BF16 if bf16_state else GDN_F32, px, *w, pz, pc, pS, pslot, rows, B,
+             _arg(out, "out", dtx, B * H * P, dev),
+             _arg(workspace, "workspace", torch.uint8, 0, dev), workspace.numel(),
+             _arg(dev_status, "dev_status", torch.int32, 1, dev))
+    return out
+
+
+class BatchTables(typing.NamedTuple):
+    """Tables of one serving step (gdn_batch_tables): cu_seqlens [N+1] int32, positions [rows]
+    int32, slot_map [rows] int64, free_head [1] int32 (pass it to the next call)."""
+    cu_seqlens: torch.Tensor
+    positions: torch.Tensor
+    slot_map: torch.Tensor
+    free_head: torch.Tensor
+
+
+def batch_tables(ctx_lens, new_lens, slot_idx, page_table, free_pages, free_head, page_size: int,
+                 num_rows: int, out: BatchTables | None = None, dev_status=None):
+    """Index tables of a serving step from the requests' lengths, built on the device.
+
+    ctx_lens [N] int32 or None (nothing cached), new_lens [N] int32, slot_idx [N] int32 or None
+    (identity), page_table [slots, max_pages] int32 (the pages that the requests lack are appended
+    to their rows, in place), free_pages [F] int32 of which those from free_head [1] on are free,
+    num_rows >= the tokens of the step.  Returns a BatchTables; rows behind the last token hold -1.
+    dev_status receives GDN_ERR_PAGES when the free list is too short (nothing is taken then)."""
+    dev = _cuda_index(new_lens, "new_lens")
+    N = new_lens.numel()
+    pn = _arg(new_lens, "new_lens", torch.int32, 0, dev)
+    pc = _arg(ctx_lens, "ctx_lens", torch.int32, N, dev)
+    ps = _arg(slot_idx, "slot_idx", torch.int32, N, dev)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [slots, max_pages] tensor")
+    slots, width = page_table.shape
+    if slot_idx is None and slots < N:
+        raise ValueError(f"page_table holds {slots} rows; the call needs {N}")
+    pt = _arg(page_table, "page_table", torch.int32, 0, dev)
+    pf = _arg(free_pages, "free_pages", torch.int32, 0, dev, True)
+    ph = _arg(free_head, "free_head", torch.int32, 1, dev, True)
+    if not new_lens.is_cuda:
+        raise ValueError("new_lens must live on a CUDA device (no CPU fallback)")
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=new_lens.device)
+        out = BatchTables(torch.empty(N + 1, **i32), torch.empty(num_rows, **i32),
+                          torch.empty(num_rows, dtype=torch.int64, device=new_lens.device),
+                          torch.empty(1, **i32))
+    _call_on(dev, "gdn_batch_tables", pc, pn, ps, slots, N, pt, width, pf, free_pages.numel(), ph,
+             page_size, num_rows, _arg(out.cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev),
+             _arg(out.positions, "positions", torch.int32, num_rows, dev),
+             _arg(out.slot_map, "slot_map", torch.int64, num_rows, dev),
+             _arg(out.free_head, "free_head (out)", torch.int32, 1, dev),
+             _arg(dev_status, "dev_status", torch.int32, 1, dev))
+    return out
+
+
 class debug_options:
     """Context manager around gdn_debug_set: the library calls of this host thread inside the
     block use the given settings; leaving the block restores the defaults.
@@ -617,4 +881,6 @@ __all__ = ["Dims", "GdnError", "lib", "conv1d_update", "gated_rmsnorm", "chunk_p
            "chunk_prefill_host", "host_plan",
            "chunk_prefill_static_ws", "STATIC_WORKSPACE_BYTES",
            "decode_step", "prefill_workspace_size", "conv_channels", "status_string", "Trace",
-           "debug_wait_probe", "debug_options", "DebugOptions", "EXPORTS", "LIB_PATH"]
+           "debug_wait_probe", "debug_options", "DebugOptions", "EXPORTS", "LIB_PATH",
+           "SsmDims", "ssm_prefill", "ssm_prefill_slots", "ssm_decode_step", "ssm_conv_channels",
+           "ssm_prefill_workspace_size", "BatchTables", "batch_tables"]

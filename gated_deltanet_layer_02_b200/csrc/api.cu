@@ -150,6 +150,7 @@ const char* gdn_status_string(int status) {
     case GDN_ERR_TIMEOUT: return "device wait timed out";
     case GDN_ERR_WORKSPACE: return "workspace too small";
     case GDN_ERR_BOUNDS: return "index check failed (bounds-check build)";
+    case GDN_ERR_PAGES: return "not enough free pages";
     default: return "unknown status";
   }
 }

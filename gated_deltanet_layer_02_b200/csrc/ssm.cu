@@ -1,0 +1,504 @@
+// ssm.cu -- selective state space layer: causal depthwise conv (width 4, bias) + SiLU, then the
+// recurrence S_t = exp(-exp(a_log) delta) S_{t-1} + delta x_t B_t^T, y_t = S_t C_t + D x_t with
+// the state [P, N] of each head in registers, and the gate silu(z) (formulas in gdn.h).
+//
+// Two kernels, the second under programmatic dependent launch:
+//   conv   u = silu(conv + bias) in fp32 for every channel ([x | B | C]) into the workspace;
+//          for single tokens it also shifts the conv history in place (each channel belongs to
+//          one thread, while the B and C channels of a group are read by all its heads).
+//   scan   one CTA per (sequence, head, 64 rows of the state): its rows are loaded before the
+//          conv has finished, take the tokens one after the other and are written once.
+#include <cuda_runtime.h>
+
+#include <utility>
+
+#include "args.cuh"
+#include "common.cuh"
+#include "tc.cuh"
+
+namespace gdn {
+
+constexpr int kScanThreads = 128;
+constexpr int kScanRows = 64;   // rows of the state per CTA (16 per warp, 8 lanes per row)
+constexpr int kConvRun = 16;    // tokens per thread of the packed conv
+
+// Tokens [s, e) of sequence n.  Entries of cu that are out of order or past T give an empty range
+// and GDN_ERR_INVALID_ARG.
+__device__ __forceinline__ void seq_range(const SsmArgs& a, int n, int& s, int& e) {
+  if (!a.cu) {
+    s = n;
+    e = n + 1;
+    return;
+  }
+  s = __ldg(a.cu + n);
+  e = __ldg(a.cu + n + 1);
+  if (s < 0 || e < s || e > a.T) {
+    report_status(a.status, GDN_ERR_INVALID_ARG);
+    s = e = 0;
+  }
+}
+
+// softplus(v) = max(v, 0) + log1p(exp(-|v|)), within [lo, hi]
+__device__ __forceinline__ float ssm_step(float v, float lo, float hi) {
+  const float sp = fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
+  return fminf(fmaxf(sp, lo), hi);
+}
+
+template <typename T>
+__device__ __forceinline__ void load8_or_zero(const T* p, float (&v)[8]) {
+  if (p) {
+    load8(p, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+  }
+}
+
+// Taps of 8 channels ([c][4] in memory) by tap, and their bias.
+template <typename T>
+__device__ __forceinline__ void load_taps(const SsmArgs& a, int c, float (&w)[4][8],
+                                          float (&b)[8]) {
+  const T* p = static_cast<const T*>(a.conv_w) + (size_t)c * 4;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float v[8];
+    load8(p + 8 * q, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e & 3][2 * q + (e >> 2)] = v[e];
+  }
+  load8_or_zero(a.conv_b ? static_cast<const T*>(a.conv_b) + c : nullptr, b);
+}
+
+// Packed prompts: a thread owns 8 channels and a run of kConvRun tokens, the three rows before
+// the current one in registers.
+template <typename T>
+__global__ void __launch_bounds__(128) ssm_conv_kernel(SsmArgs a) {
+  pdl_trigger();
+  const int c = (blockIdx.y * 128 + threadIdx.x) * 8, t0 = blockIdx.x * kConvRun;
+  if (c >= a.Cc) return;
+  float w[4][8], b[8];
+  load_taps<T>(a, c, w, b);
+  const T* x = static_cast<const T*>(a.x) + c;
+  const T* c0 = static_cast<const T*>(a.conv0);
+  float h[3][8];
+  int n = seq_of_token(a.cu, a.N, t0) - 1, s = 0, end = 0;
+  const int t1 = min(a.T, t0 + kConvRun);
+  bool fresh = true;  // the history registers do not hold the rows before t
+  for (int t = t0; t < t1; ++t) {
+    while (n < a.N && t >= end) {  // the next sequence that may hold t
+      ++n;
+      if (n < a.N) seq_range(a, n, s, end);
+      fresh = true;
+    }
+    if (n >= a.N || t < s) continue;  // behind the last sequence
+    if (fresh) {
+      const int row = state_row(a.slot, n, a.num_slots);
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const int r = t - 3 + j;
+        load8_or_zero(r >= s ? x + (size_t)r * a.Cc
+                             : (c0 && row >= 0 ? c0 + ((size_t)row * 3 + 3 + r - s) * a.Cc + c
+                                               : nullptr),
+                      h[j]);
+      }
+      fresh = false;
+    }
+    float v[8], out[8];
+    load8(x + (size_t)t * a.Cc, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      out[e] = silu_f(fmaf(w[3][e], v[e],
+                           fmaf(w[2][e], h[2][e], fmaf(w[1][e], h[1][e], fmaf(w[0][e], h[0][e], b[e])))));
+      h[0][e] = h[1][e];
+      h[1][e] = h[2][e];
+      h[2][e] = v[e];
+    }
+    store8(a.u + (size_t)t * a.Cc + c, out);
+  }
+}
+
+// One token per sequence: a thread owns 8 channels of one sequence and shifts their history.
+template <typename T>
+__global__ void __launch_bounds__(128) ssm_conv_step_kernel(SsmArgs a) {
+  pdl_trigger();
+  const int c = (blockIdx.x * 128 + threadIdx.x) * 8, n = blockIdx.y;
+  if (c >= a.Cc) return;
+  const int row = state_row(a.slot, n, a.num_slots);
+  if (row < 0) {  // slot out of range: the sequence is skipped
+    if (c == 0) report_status(a.status, GDN_ERR_INVALID_ARG);
+    return;
+  }
+  float w[4][8], b[8], h[4][8], out[8];
+  T* cs = static_cast<T*>(a.convN) + (size_t)row * 3 * a.Cc + c;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) load8(cs + (size_t)j * a.Cc, h[j]);
+  load8(static_cast<const T*>(a.x) + (size_t)n * a.Cc + c, h[3]);
+  load_taps<T>(a, c, w, b);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    out[e] = silu_f(fmaf(w[3][e], h[3][e],
+                         fmaf(w[2][e], h[2][e], fmaf(w[1][e], h[1][e], fmaf(w[0][e], h[0][e], b[e])))));
+#pragma unroll
+  for (int j = 0; j < 3; ++j) store8(cs + (size_t)j * a.Cc, h[j + 1]);
+  store8(a.u + (size_t)n * a.Cc + c, out);
+}
+
+// Final conv history of sequence n (tokens [s, end), pool row `row`): the last three rows of its
+// history followed by its tokens.  Block k of the sequence's nb blocks takes its share of the
+// channels; a thread reads its 8 channels before it writes them, so convN may be conv0 (the conv,
+// which reads conv0 too, has finished).
+template <typename T>
+__device__ __forceinline__ void conv_history(const SsmArgs& a, int n, int row, int s, int end,
+                                             int k, int nb) {
+  if (!a.convN || row < 0) return;
+  const T* c0 = static_cast<const T*>(a.conv0);
+  for (int c = (k * (int)blockDim.x + (int)threadIdx.x) * 8; c < a.Cc;
+       c += nb * (int)blockDim.x * 8) {
+    float r[3][8];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const int t = end - 3 + j;  // may lie before the sequence
+      load8_or_zero(t >= s ? static_cast<const T*>(a.x) + (size_t)t * a.Cc + c
+                           : (c0 ? c0 + ((size_t)row * 3 + 3 + t - s) * a.Cc + c : nullptr),
+                    r[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      store8(static_cast<T*>(a.convN) + ((size_t)row * 3 + j) * a.Cc + c, r[j]);
+  }
+}
+
+// Four consecutive elements of a state row.
+__device__ __forceinline__ float4 load4(const float* p) {
+  return __ldcs(reinterpret_cast<const float4*>(p));
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 r = __ldcs(reinterpret_cast<const uint2*>(p));
+  const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.x));
+  const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.y));
+  return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+__device__ __forceinline__ void store4(float* p, float4 v) {
+  __stcs(reinterpret_cast<float4*>(p), v);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)));
+}
+
+// Lane `sub` of a row's eight lanes holds columns 4 sub + 32 m + e (m < NS / 32).  Warp w owns
+// rows 16 w + 4 q + lane / 8 (q < 4) of the CTA's 64.
+template <typename T, typename TS, int NS>
+__global__ void __launch_bounds__(kScanThreads, 4) ssm_scan_kernel(SsmArgs a) {
+  constexpr int M = NS / 32;
+  pdl_trigger();
+  const int blocks = a.P / kScanRows;
+  const int pb = blockIdx.x % blocks, h = (blockIdx.x / blocks) % a.H;
+  const int n = blockIdx.x / (blocks * a.H);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grp = lane >> 3, sub = lane & 7;
+  const int row = state_row(a.slot, n, a.num_slots);
+  if (row < 0) {
+    if (tid == 0) report_status(a.status, GDN_ERR_INVALID_ARG);
+    if (!a.cu) return;  // a decode step skips the sequence; a prompt starts from zero
+  }
+  int s, end;
+  seq_range(a, n, s, end);
+  const int p0 = pb * kScanRows + warp * 16 + grp;  // this lane group's rows: p0 + 4 q
+  const size_t sbase = (((size_t)(row < 0 ? 0 : row) * a.H + h) * a.P + p0) * NS + 4 * sub;
+  float4 f[4][M];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+      f[q][m] = a.S0 && row >= 0
+                    ? load4(static_cast<const TS*>(a.S0) + sbase + (size_t)(4 * q) * NS + 32 * m)
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float rate = -expf(a.a_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  const float D = a.D ? a.D[h] : 0.f;
+  const int cB = a.H * a.P + (h / (a.H / a.G)) * NS + 4 * sub, cC = cB + a.G * NS;
+  const int cx = h * a.P + p0;
+  pdl_wait();  // the conv outputs
+  for (int t = s; t < end; ++t) {
+    const float* u = a.u + (size_t)t * a.Cc;
+    const float delta = ssm_step(a.dt[(size_t)t * a.H + h] + bias, a.dt_min, a.dt_max);
+    const float alpha = expf(rate * delta);
+    float4 B[M], C[M];
+    float xv[4], o[4];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      B[m] = *reinterpret_cast<const float4*>(u + cB + 32 * m);
+      C[m] = *reinterpret_cast<const float4*>(u + cC + 32 * m);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) xv[q] = u[cx + 4 * q];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float dx = delta * xv[q];
+      float acc = 0.f;
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        float4& r = f[q][m];
+        r.x = fmaf(alpha, r.x, dx * B[m].x);
+        r.y = fmaf(alpha, r.y, dx * B[m].y);
+        r.z = fmaf(alpha, r.z, dx * B[m].z);
+        r.w = fmaf(alpha, r.w, dx * B[m].w);
+        acc = fmaf(r.x, C[m].x, fmaf(r.y, C[m].y, fmaf(r.z, C[m].z, fmaf(r.w, C[m].w, acc))));
+      }
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+      o[q] = fmaf(D, xv[q], acc);
+    }
+    if (sub < 4) {  // lane `sub` writes row 4 sub of its group's four
+      float y = sub == 0 ? o[0] : (sub == 1 ? o[1] : (sub == 2 ? o[2] : o[3]));
+      const size_t at = ((size_t)t * a.H + h) * a.P + p0 + 4 * sub;
+      if (a.z) y *= silu_f(to_f(static_cast<const T*>(a.z)[at]));
+      static_cast<T*>(a.out)[at] = from_f<T>(y);
+    }
+  }
+  if (a.cu) conv_history<T>(a, n, row, s, end, blockIdx.x % (blocks * a.H), blocks * a.H);
+  if (a.SN && row >= 0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        store4(static_cast<TS*>(a.SN) + sbase + (size_t)(4 * q) * NS + 32 * m, f[q][m]);
+  }
+}
+
+}  // namespace gdn
+
+namespace gdn_host {
+
+template <typename K>
+static cudaError_t launch_ssm(bool pdl, K kern, dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                              const gdn::SsmArgs& a, const char* name) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = (pdl && !trace_attached()) ? 1 : 0;
+  trace_begin(name, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  trace_end(s);
+  return e;
+}
+
+template <typename T, typename TS>
+static cudaError_t launch_scan(const gdn::SsmArgs& a, int NS, const char* name, cudaStream_t s) {
+  const bool pdl = a.T > 0;  // behind a conv of this call; alone, it is an ordinary launch
+  const dim3 grid((unsigned)a.N * a.H * (a.P / gdn::kScanRows)), block(gdn::kScanThreads);
+  return NS == 128 ? launch_ssm(pdl, gdn::ssm_scan_kernel<T, TS, 128>, grid, block, 0, s, a, name)
+                   : launch_ssm(pdl, gdn::ssm_scan_kernel<T, TS, 64>, grid, block, 0, s, a, name);
+}
+
+static cudaError_t launch_ssm_prefill(bool bf16, const gdn::SsmArgs& a, int NS, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (a.T > 0) {
+    const dim3 grid((a.T + gdn::kConvRun - 1) / gdn::kConvRun, (a.Cc / 8 + 127) / 128);
+    e = bf16 ? launch_ssm(false, gdn::ssm_conv_kernel<__nv_bfloat16>, grid, dim3(128), 0, s, a,
+                          "ssm_conv")
+             : launch_ssm(false, gdn::ssm_conv_kernel<float>, grid, dim3(128), 0, s, a, "ssm_conv");
+    if (e != cudaSuccess) return e;
+  }
+  return bf16 ? launch_scan<__nv_bfloat16, float>(a, NS, "ssm_scan", s)
+              : launch_scan<float, float>(a, NS, "ssm_scan", s);
+}
+
+static cudaError_t launch_ssm_decode(bool bf16, bool state_bf16, const gdn::SsmArgs& a, int NS,
+                                     cudaStream_t s) {
+  const dim3 grid((a.Cc / 8 + 127) / 128, a.N);
+  const char* name = state_bf16 ? "ssm_decode_step_bf16_state" : "ssm_decode_step";
+  cudaError_t e =
+      bf16 ? launch_ssm(false, gdn::ssm_conv_step_kernel<__nv_bfloat16>, grid, dim3(128), 0, s, a,
+                        "ssm_conv_step")
+           : launch_ssm(false, gdn::ssm_conv_step_kernel<float>, grid, dim3(128), 0, s, a,
+                        "ssm_conv_step");
+  if (e != cudaSuccess) return e;
+  if (bf16)
+    return state_bf16 ? launch_scan<__nv_bfloat16, __nv_bfloat16>(a, NS, name, s)
+                      : launch_scan<__nv_bfloat16, float>(a, NS, name, s);
+  return state_bf16 ? launch_scan<float, __nv_bfloat16>(a, NS, name, s)
+                    : launch_scan<float, float>(a, NS, name, s);
+}
+
+}  // namespace gdn_host
+
+namespace {
+
+bool misaligned(const void* p, uintptr_t to = 16) {
+  return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0;
+}
+
+int64_t ssm_channels(const gdn_ssm_dims* d) {
+  return (int64_t)d->num_heads * d->head_dim + 2 * (int64_t)d->num_groups * d->state_dim;
+}
+
+int check_ssm_dims(const gdn_ssm_dims* d) {
+  if (!d) return GDN_ERR_INVALID_ARG;
+  if (d->num_heads <= 0 || d->num_groups <= 0 || d->head_dim <= 0 || d->state_dim <= 0 ||
+      d->conv_kernel <= 0 || d->num_heads % d->num_groups != 0)
+    return GDN_ERR_INVALID_ARG;
+  if (!(d->dt_min >= 0.f) || !(d->dt_max >= d->dt_min)) return GDN_ERR_INVALID_ARG;
+  if ((d->head_dim != 64 && d->head_dim != 128) || (d->state_dim != 64 && d->state_dim != 128) ||
+      d->conv_kernel != gdn::kConvK)
+    return GDN_ERR_UNSUPPORTED;
+  if (ssm_channels(d) > (1 << 20)) return GDN_ERR_UNSUPPORTED;  // 32-bit channel indices
+  return GDN_OK;
+}
+
+bool ssm_dtype_ok(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16; }
+
+gdn::SsmArgs ssm_args(const gdn_ssm_dims* d) {
+  gdn::SsmArgs a{};
+  a.H = d->num_heads;
+  a.G = d->num_groups;
+  a.P = d->head_dim;
+  a.Cc = (int)ssm_channels(d);
+  a.dt_min = d->dt_min;
+  a.dt_max = d->dt_max;
+  return a;
+}
+
+int ssm_prefill_impl(const gdn_ssm_dims* dims, gdn_dtype dtype, const void* x, const void* conv_w,
+                     const void* conv_b, const float* dt, const float* dt_bias, const float* a_log,
+                     const float* D, const void* z, const int32_t* cu, int32_t N, int32_t T,
+                     const int32_t* slot, int32_t num_slots, const float* S0, float* SN,
+                     const void* conv0, void* convN, void* out, void* workspace,
+                     size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  int rc = check_ssm_dims(dims);
+  if (rc) return rc;
+  if (!ssm_dtype_ok(dtype)) return GDN_ERR_UNSUPPORTED;
+  if (N < 0 || T < 0 || (N == 0 && T > 0)) return GDN_ERR_INVALID_ARG;
+  if (N > 0 && (!cu || !a_log)) return GDN_ERR_INVALID_ARG;
+  if (T > 0 && (!x || !conv_w || !dt || !out)) return GDN_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, conv_w, conv_b, dt, dt_bias, a_log, D, z, S0, SN, conv0, convN, out};
+  for (const void* p : ptrs)
+    if (p && misaligned(p)) return GDN_ERR_INVALID_ARG;
+  if (workspace && misaligned(workspace, 256)) return GDN_ERR_INVALID_ARG;
+  // the grid covers every (sequence, head, 64 rows)
+  if ((int64_t)N * dims->num_heads * (dims->head_dim / gdn::kScanRows) > INT32_MAX)
+    return GDN_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < gdn_ssm_prefill_workspace_size(dims, dtype, N, T))
+    return GDN_ERR_WORKSPACE;
+  if (N == 0) return GDN_OK;
+  gdn::SsmArgs a = ssm_args(dims);
+  a.x = x;
+  a.conv_w = conv_w;
+  a.conv_b = conv_b;
+  a.dt = dt;
+  a.dt_bias = dt_bias;
+  a.a_log = a_log;
+  a.D = D;
+  a.z = z;
+  a.cu = cu;
+  a.S0 = S0;
+  a.SN = SN;
+  a.conv0 = conv0;
+  a.convN = convN;
+  a.out = out;
+  a.slot = slot;
+  a.status = dev_status;
+  a.u = static_cast<float*>(workspace);
+  a.num_slots = num_slots;
+  a.N = N;
+  a.T = T;
+  return gdn_host::launch_ssm_prefill(dtype == GDN_BF16, a, dims->state_dim,
+                                      static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gdn_ssm_conv_channels(const gdn_ssm_dims* dims) { return dims ? ssm_channels(dims) : -1; }
+
+size_t gdn_ssm_prefill_workspace_size(const gdn_ssm_dims* dims, gdn_dtype dtype, int32_t num_seqs,
+                                      int32_t num_tokens) {
+  if (check_ssm_dims(dims) != GDN_OK || !ssm_dtype_ok(dtype) || num_seqs < 0 || num_tokens < 0)
+    return 0;
+  return 256 + (size_t)num_tokens * ssm_channels(dims) * 4;
+}
+
+int gdn_ssm_prefill(const gdn_ssm_dims* dims, gdn_dtype dtype, const void* x, const void* conv_w,
+                    const void* conv_b, const float* dt, const float* dt_bias, const float* a_log,
+                    const float* D, const void* z, const int32_t* cu_seqlens, int32_t num_seqs,
+                    int32_t num_tokens, const float* S0, float* SN, const void* conv0, void* convN,
+                    void* out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                    void* stream) {
+  return ssm_prefill_impl(dims, dtype, x, conv_w, conv_b, dt, dt_bias, a_log, D, z, cu_seqlens,
+                          num_seqs, num_tokens, nullptr, num_seqs, S0, SN, conv0, convN, out,
+                          workspace, workspace_bytes, dev_status, stream);
+}
+
+int gdn_ssm_prefill_slots(const gdn_ssm_dims* dims, gdn_dtype dtype, const void* x,
+                          const void* conv_w, const void* conv_b, const float* dt,
+                          const float* dt_bias, const float* a_log, const float* D, const void* z,
+                          const int32_t* cu_seqlens, int32_t num_seqs, int32_t num_tokens,
+                          const int32_t* slot_idx, int32_t num_slots, float* S_pool,
+                          void* conv_pool, void* out, void* workspace, size_t workspace_bytes,
+                          int32_t* dev_status, void* stream) {
+  if (num_seqs > 0 && !S_pool) return GDN_ERR_INVALID_ARG;
+  if (num_slots < 0 || (!slot_idx && num_slots < num_seqs)) return GDN_ERR_INVALID_ARG;
+  return ssm_prefill_impl(dims, dtype, x, conv_w, conv_b, dt, dt_bias, a_log, D, z, cu_seqlens,
+                          num_seqs, num_tokens, slot_idx, num_slots, S_pool, S_pool, conv_pool,
+                          conv_pool, out, workspace, workspace_bytes, dev_status, stream);
+}
+
+size_t gdn_ssm_decode_workspace_size(const gdn_ssm_dims* dims, int32_t batch) {
+  if (check_ssm_dims(dims) != GDN_OK || batch < 0) return 0;
+  return 256 + (size_t)batch * ssm_channels(dims) * 4;
+}
+
+int gdn_ssm_decode_step(const gdn_ssm_dims* dims, gdn_dtype dtype, gdn_dtype state_dtype,
+                        const void* x, const void* conv_w, const void* conv_b, const float* dt,
+                        const float* dt_bias, const float* a_log, const float* D, const void* z,
+                        void* conv_state, void* S, const int32_t* slot_idx, int32_t num_slots,
+                        int32_t batch, void* out, void* workspace, size_t workspace_bytes,
+                        int32_t* dev_status, void* stream) {
+  int rc = check_ssm_dims(dims);
+  if (rc) return rc;
+  if (!ssm_dtype_ok(dtype) || !ssm_dtype_ok(state_dtype)) return GDN_ERR_UNSUPPORTED;
+  if (batch < 0) return GDN_ERR_INVALID_ARG;
+  if (num_slots < 0 || (!slot_idx && num_slots < batch)) return GDN_ERR_INVALID_ARG;
+  if (batch > 0 && (!x || !conv_w || !dt || !a_log || !conv_state || !S || !out))
+    return GDN_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, conv_w, conv_b, dt, dt_bias, a_log, D, z, conv_state, S, out};
+  for (const void* p : ptrs)
+    if (p && misaligned(p)) return GDN_ERR_INVALID_ARG;
+  if (workspace && misaligned(workspace, 256)) return GDN_ERR_INVALID_ARG;
+  if (batch > 65535) return GDN_ERR_UNSUPPORTED;  // the conv kernel's grid
+  if (batch == 0) return GDN_OK;
+  if (!workspace || workspace_bytes < gdn_ssm_decode_workspace_size(dims, batch))
+    return GDN_ERR_WORKSPACE;
+  gdn::SsmArgs a = ssm_args(dims);
+  a.x = x;
+  a.conv_w = conv_w;
+  a.conv_b = conv_b;
+  a.dt = dt;
+  a.dt_bias = dt_bias;
+  a.a_log = a_log;
+  a.D = D;
+  a.z = z;
+  a.S0 = S;
+  a.SN = S;
+  a.convN = conv_state;
+  a.out = out;
+  a.slot = slot_idx;
+  a.status = dev_status;
+  a.u = static_cast<float*>(workspace);
+  a.num_slots = num_slots;
+  a.N = a.T = batch;
+  return gdn_host::launch_ssm_decode(dtype == GDN_BF16, state_dtype == GDN_BF16, a,
+                                     dims->state_dim,
+                                     static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -56,9 +56,11 @@ typedef enum gdn_status {
   GDN_ERR_CUDA = -3,        /* a CUDA runtime call or kernel launch failed */
   GDN_ERR_TIMEOUT = -4,     /* written to dev_status by a device wait that ran out */
   GDN_ERR_WORKSPACE = -5,   /* workspace missing or smaller than *_workspace_size() */
-  GDN_ERR_BOUNDS = -6       /* bounds-check build only (libgdn_checked.so, compiled with
+  GDN_ERR_BOUNDS = -6,      /* bounds-check build only (libgdn_checked.so, compiled with
                                -DGDN_BOUNDS_CHECK): a kernel index check failed and the access
                                was skipped; never reported by the normal build */
+  GDN_ERR_PAGES = -7        /* written to dev_status by gdn_batch_tables: the free list holds
+                               fewer pages than the batch needs (nothing was taken) */
 } gdn_status;
 
 typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
@@ -324,6 +326,126 @@ int gdn_decode_step_bf16_state(const gdn_dims* dims, gdn_dtype dtype, const void
                                const void* z, const void* norm_w, void* conv_state, void* S,
                                const int32_t* slot_idx, int32_t num_slots, int32_t batch,
                                void* out, int32_t* dev_status, void* stream);
+
+/*
+ * The selective state space layer (scalar decay per head): the other linear recurrence served
+ * from a conv state and a matrix state per head, over the same packed sequences and state pools
+ * as the Gated DeltaNet calls.  Per token t of a sequence and head h (group g = h / (H/G)), with
+ * the input row [x (H P) | B (G N) | C (G N)]:
+ *   u_t   = silu(sum_i conv_w[c, i] row_{t-K+1+i}[c] + conv_b[c])     (depthwise, causal)
+ *   delta = min(max(softplus(dt[t, h] + dt_bias[h]), dt_min), dt_max)
+ *   S_t   = exp(-exp(a_log[h]) delta) S_{t-1} + delta x_t B_t^T
+ *   y_t   = S_t C_t + D[h] x_t
+ *   out_t = y_t silu(z_t)                                             (when z is given)
+ * The RMSNorm of a layer that has one is a call of its own: gdn_gated_rmsnorm on the rows of a
+ * call without z.  Rules of the file header apply; in addition every index that comes from
+ * device memory (cu_seqlens, slot_idx) is checked on the device in every build: a sequence whose
+ * cu_seqlens entries are out of order or past num_tokens counts as empty and sets dev_status to
+ * GDN_ERR_INVALID_ARG.  Rows of `out` at and behind cu[N] are left as they were.
+ */
+typedef struct gdn_ssm_dims {
+  int32_t num_heads;   /* H: a multiple of num_groups */
+  int32_t num_groups;  /* G: groups of heads that share B and C */
+  int32_t head_dim;    /* P: 64 or 128 */
+  int32_t state_dim;   /* N: 64 or 128 */
+  int32_t conv_kernel; /* K: 4 */
+  float dt_min;        /* bounds of delta (0 and infinity: none) */
+  float dt_max;
+} gdn_ssm_dims;
+
+/* Conv channel count H P + 2 G N, in the order [x | B | C]. */
+int64_t gdn_ssm_conv_channels(const gdn_ssm_dims* dims);
+
+/*
+ * gdn_ssm_prefill -- the layer over packed variable-length sequences.
+ *   x        [T, Cc]          pre-conv rows
+ *   conv_w   [Cc, K]          tap K-1 multiplies the current token
+ *   conv_b   [Cc]             nullable: no bias
+ *   dt       [T, H] fp32      step before the bias and the softplus
+ *   dt_bias  [H] fp32         nullable: zeros
+ *   a_log    [H] fp32
+ *   D        [H] fp32         nullable: no direct term
+ *   z        [T, H, P]        nullable: no gate (out = y)
+ *   cu_seqlens [N+1] int32    device, as for gdn_conv1d_update; cu[N] may be below num_tokens
+ *   S0, SN   [N, H, P, N] fp32  nullable: zero initial states / no final states (may be equal)
+ *   conv0, convN [N, K-1, Cc]   nullable, as for gdn_chunk_prefill (may be equal)
+ *   out      [T, H, P]
+ *   workspace: at least gdn_ssm_prefill_workspace_size() bytes, 256-byte aligned.
+ *   dev_status int32, nullable.
+ */
+size_t gdn_ssm_prefill_workspace_size(const gdn_ssm_dims* dims, gdn_dtype dtype, int32_t num_seqs,
+                                      int32_t num_tokens);
+int gdn_ssm_prefill(const gdn_ssm_dims* dims, gdn_dtype dtype, const void* x, const void* conv_w,
+                    const void* conv_b, const float* dt, const float* dt_bias, const float* a_log,
+                    const float* D, const void* z, const int32_t* cu_seqlens, int32_t num_seqs,
+                    int32_t num_tokens, const float* S0, float* SN, const void* conv0, void* convN,
+                    void* out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                    void* stream);
+
+/*
+ * gdn_ssm_prefill_slots -- gdn_ssm_prefill with the states in pools shared with
+ * gdn_ssm_decode_step: sequence n starts from and overwrites rows slot_idx[n] of S_pool
+ * [slots, H, P, N] fp32 (required when N > 0) and conv_pool [slots, K-1, Cc] (nullable: zero
+ * history, none kept).  slot_idx, num_slots and what happens to a slot outside the pool: as
+ * gdn_chunk_prefill_slots.
+ */
+int gdn_ssm_prefill_slots(const gdn_ssm_dims* dims, gdn_dtype dtype, const void* x,
+                          const void* conv_w, const void* conv_b, const float* dt,
+                          const float* dt_bias, const float* a_log, const float* D, const void* z,
+                          const int32_t* cu_seqlens, int32_t num_seqs, int32_t num_tokens,
+                          const int32_t* slot_idx, int32_t num_slots, float* S_pool,
+                          void* conv_pool, void* out, void* workspace, size_t workspace_bytes,
+                          int32_t* dev_status, void* stream);
+
+/*
+ * gdn_ssm_decode_step -- one token for each of B sequences, conv and recurrent state in place.
+ *   x [B, Cc], dt [B, H] fp32, z [B, H, P] nullable, out [B, H, P]; weights as gdn_ssm_prefill;
+ *   conv_state [slots, K-1, Cc] and S [slots, H, P, N] in/out; state_dtype: type of S (GDN_F32, or
+ *   GDN_BF16: read, updated in fp32 and rounded to nearest even once when written back);
+ *   slot_idx [B] int32 nullable, num_slots, skipped slots, dev_status: as gdn_decode_step.
+ *   workspace: at least gdn_ssm_decode_workspace_size() bytes, 256-byte aligned (the conv outputs
+ *   of the step, fp32); calls that may overlap on the GPU need one each.
+ */
+size_t gdn_ssm_decode_workspace_size(const gdn_ssm_dims* dims, int32_t batch);
+int gdn_ssm_decode_step(const gdn_ssm_dims* dims, gdn_dtype dtype, gdn_dtype state_dtype,
+                        const void* x, const void* conv_w, const void* conv_b, const float* dt,
+                        const float* dt_bias, const float* a_log, const float* D, const void* z,
+                        void* conv_state, void* S, const int32_t* slot_idx, int32_t num_slots,
+                        int32_t batch, void* out, void* workspace, size_t workspace_bytes,
+                        int32_t* dev_status, void* stream);
+
+/*
+ * gdn_batch_tables -- the index tables of one serving step, from the requests' lengths, in one
+ * launch and without a copy to the host.
+ * Source: the "Qwen3-Next" SGLang cookbook, section 3.2 (a state slot per request and a paged
+ * cache with --page-size beside it).  Request n has ctx_lens[n] tokens in the cache, brings
+ * new_lens[n] more, and owns row slot_idx[n] of page_table, whose first ceil(ctx / page_size)
+ * entries name the pages it holds.
+ *   ctx_lens  [N] int32 nullable (= zeros); new_lens [N] int32
+ *   slot_idx  [N] int32 nullable (= identity); the slots of one call must be distinct
+ *   page_table [num_slots, max_pages] int32 in/out: the pages the request lacks are appended to
+ *             its row, the rest of the table is left as it was
+ *   free_pages [num_free] int32, free_head [1] int32: free_pages[free_head ...] are free; they are
+ *             taken from the front, request by request
+ *   page_size >= 1, in tokens
+ *   num_rows  rows of positions and slot_map (at least the sum of new_lens; a padded batch has more)
+ *   cu_seqlens [N+1] int32 out: prefix sums of new_lens, as every prefill call takes them
+ *   positions [num_rows] int32 out, nullable: ctx_lens[n] + j for token j of request n
+ *   slot_map  [num_rows] int64 out, nullable: cache row page * page_size + position % page_size
+ *   free_head_out [1] int32 out: free_head plus the pages taken; may not be free_head itself
+ *   Rows behind the last token get -1 in positions and slot_map.
+ * A request with a negative length, a slot outside [0, num_slots), more pages than max_pages or a
+ * position past 2^31 - 1 counts as bringing no token and sets dev_status to GDN_ERR_INVALID_ARG;
+ * a negative page number of a page it holds gives slot_map -1 and the same status.  When the free
+ * list is too short (GDN_ERR_PAGES), num_rows is too small or free_head lies outside
+ * [0, num_free] (GDN_ERR_INVALID_ARG), nothing is taken: cu_seqlens is all zeros, every row -1, the
+ * table and the head as they were.
+ */
+int gdn_batch_tables(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* slot_idx,
+                     int32_t num_slots, int32_t num_reqs, int32_t* page_table, int32_t max_pages,
+                     const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
+                     int32_t page_size, int32_t num_rows, int32_t* cu_seqlens, int32_t* positions,
+                     int64_t* slot_map, int32_t* free_head_out, int32_t* dev_status, void* stream);
 
 /*
  * gdn_chunk_prefill_static_ws -- gdn_chunk_prefill for callers that cannot allocate device
