@@ -14,6 +14,7 @@
 
 #include "args.cuh"
 #include "common.cuh"
+#include "ssm.cuh"
 #include "tc.cuh"
 
 namespace gdn {
@@ -21,53 +22,6 @@ namespace gdn {
 constexpr int kScanThreads = 128;
 constexpr int kScanRows = 64;   // rows of the state per CTA (16 per warp, 8 lanes per row)
 constexpr int kConvRun = 16;    // tokens per thread of the packed conv
-
-// Tokens [s, e) of sequence n.  Entries of cu that are out of order or past T give an empty range
-// and GDN_ERR_INVALID_ARG.
-__device__ __forceinline__ void seq_range(const SsmArgs& a, int n, int& s, int& e) {
-  if (!a.cu) {
-    s = n;
-    e = n + 1;
-    return;
-  }
-  s = __ldg(a.cu + n);
-  e = __ldg(a.cu + n + 1);
-  if (s < 0 || e < s || e > a.T) {
-    report_status(a.status, GDN_ERR_INVALID_ARG);
-    s = e = 0;
-  }
-}
-
-// softplus(v) = max(v, 0) + log1p(exp(-|v|)), within [lo, hi]
-__device__ __forceinline__ float ssm_step(float v, float lo, float hi) {
-  const float sp = fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
-  return fminf(fmaxf(sp, lo), hi);
-}
-
-template <typename T>
-__device__ __forceinline__ void load8_or_zero(const T* p, float (&v)[8]) {
-  if (p) {
-    load8(p, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-  }
-}
-
-// Taps of 8 channels ([c][4] in memory) by tap, and their bias.
-template <typename T>
-__device__ __forceinline__ void load_taps(const SsmArgs& a, int c, float (&w)[4][8],
-                                          float (&b)[8]) {
-  const T* p = static_cast<const T*>(a.conv_w) + (size_t)c * 4;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float v[8];
-    load8(p + 8 * q, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e & 3][2 * q + (e >> 2)] = v[e];
-  }
-  load8_or_zero(a.conv_b ? static_cast<const T*>(a.conv_b) + c : nullptr, b);
-}
 
 // Packed prompts: a thread owns 8 channels and a run of kConvRun tokens, the three rows before
 // the current one in registers.
@@ -143,31 +97,6 @@ __global__ void __launch_bounds__(128) ssm_conv_step_kernel(SsmArgs a) {
   store8(a.u + (size_t)n * a.Cc + c, out);
 }
 
-// Final conv history of sequence n (tokens [s, end), pool row `row`): the last three rows of its
-// history followed by its tokens.  Block k of the sequence's nb blocks takes its share of the
-// channels; a thread reads its 8 channels before it writes them, so convN may be conv0 (the conv,
-// which reads conv0 too, has finished).
-template <typename T>
-__device__ __forceinline__ void conv_history(const SsmArgs& a, int n, int row, int s, int end,
-                                             int k, int nb) {
-  if (!a.convN || row < 0) return;
-  const T* c0 = static_cast<const T*>(a.conv0);
-  for (int c = (k * (int)blockDim.x + (int)threadIdx.x) * 8; c < a.Cc;
-       c += nb * (int)blockDim.x * 8) {
-    float r[3][8];
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      const int t = end - 3 + j;  // may lie before the sequence
-      load8_or_zero(t >= s ? static_cast<const T*>(a.x) + (size_t)t * a.Cc + c
-                           : (c0 ? c0 + ((size_t)row * 3 + 3 + t - s) * a.Cc + c : nullptr),
-                    r[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-      store8(static_cast<T*>(a.convN) + ((size_t)row * 3 + j) * a.Cc + c, r[j]);
-  }
-}
-
 // Four consecutive elements of a state row.
 __device__ __forceinline__ float4 load4(const float* p) {
   return __ldcs(reinterpret_cast<const float4*>(p));
@@ -198,7 +127,10 @@ __global__ void __launch_bounds__(kScanThreads, 4) ssm_scan_kernel(SsmArgs a) {
   const int row = state_row(a.slot, n, a.num_slots);
   if (row < 0) {
     if (tid == 0) report_status(a.status, GDN_ERR_INVALID_ARG);
-    if (!a.cu) return;  // a decode step skips the sequence; a prompt starts from zero
+    if (!a.cu) {  // a decode step skips the sequence; a prompt starts from zero
+      pdl_wait();
+      return;
+    }
   }
   int s, end;
   seq_range(a, n, s, end);
@@ -295,8 +227,17 @@ static cudaError_t launch_scan(const gdn::SsmArgs& a, int NS, const char* name, 
                    : launch_ssm(pdl, gdn::ssm_scan_kernel<T, TS, 64>, grid, block, 0, s, a, name);
 }
 
+cudaError_t launch_ssm_tc(gdn::SsmTcArgs g, void* workspace, cudaStream_t s);
+size_t ssm_tc_workspace(int N, int T, int H, int G, int P, int NS, int Cc);
+
 static cudaError_t launch_ssm_prefill(bool bf16, const gdn::SsmArgs& a, int NS, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
+  if (bf16 && a.T > 0) {
+    gdn::SsmTcArgs g{};
+    g.a = a;
+    g.NS = NS;
+    return launch_ssm_tc(g, a.u, s);
+  }
   if (a.T > 0) {
     const dim3 grid((a.T + gdn::kConvRun - 1) / gdn::kConvRun, (a.Cc / 8 + 127) / 128);
     e = bf16 ? launch_ssm(false, gdn::ssm_conv_kernel<__nv_bfloat16>, grid, dim3(128), 0, s, a,
@@ -379,8 +320,8 @@ int ssm_prefill_impl(const gdn_ssm_dims* dims, gdn_dtype dtype, const void* x, c
   for (const void* p : ptrs)
     if (p && misaligned(p)) return GDN_ERR_INVALID_ARG;
   if (workspace && misaligned(workspace, 256)) return GDN_ERR_INVALID_ARG;
-  // the grid covers every (sequence, head, 64 rows)
-  if ((int64_t)N * dims->num_heads * (dims->head_dim / gdn::kScanRows) > INT32_MAX)
+  // a grid covers every (sequence or chunk, head, 64 rows)
+  if (((int64_t)N + T / 128) * dims->num_heads * (dims->head_dim / gdn::kScanRows) > INT32_MAX)
     return GDN_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < gdn_ssm_prefill_workspace_size(dims, dtype, N, T))
     return GDN_ERR_WORKSPACE;
@@ -422,6 +363,10 @@ size_t gdn_ssm_prefill_workspace_size(const gdn_ssm_dims* dims, gdn_dtype dtype,
                                       int32_t num_tokens) {
   if (check_ssm_dims(dims) != GDN_OK || !ssm_dtype_ok(dtype) || num_seqs < 0 || num_tokens < 0)
     return 0;
+  if (dtype == GDN_BF16)
+    return 256 + gdn_host::ssm_tc_workspace(num_seqs, num_tokens, dims->num_heads,
+                                            dims->num_groups, dims->head_dim, dims->state_dim,
+                                            (int)ssm_channels(dims));
   return 256 + (size_t)num_tokens * ssm_channels(dims) * 4;
 }
 

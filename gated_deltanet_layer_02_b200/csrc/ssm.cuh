@@ -1,0 +1,95 @@
+// ssm.cuh -- parts shared by the kernels of the state space layer (ssm.cu, ssm_tc.cu).
+#pragma once
+#include <cuda_fp16.h>
+
+#include "args.cuh"
+#include "common.cuh"
+
+namespace gdn {
+
+// Tokens [s, e) of sequence n.  Entries of cu that are out of order or past T give an empty range
+// and GDN_ERR_INVALID_ARG.
+__device__ __forceinline__ void seq_range(const SsmArgs& a, int n, int& s, int& e) {
+  if (!a.cu) {
+    s = n;
+    e = n + 1;
+    return;
+  }
+  s = __ldg(a.cu + n);
+  e = __ldg(a.cu + n + 1);
+  if (s < 0 || e < s || e > a.T) {
+    report_status(a.status, GDN_ERR_INVALID_ARG);
+    s = e = 0;
+  }
+}
+
+// softplus(v) = max(v, 0) + log1p(exp(-|v|)), within [lo, hi]
+__device__ __forceinline__ float ssm_step(float v, float lo, float hi) {
+  const float sp = fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
+  return fminf(fmaxf(sp, lo), hi);
+}
+
+template <typename T>
+__device__ __forceinline__ void load8_or_zero(const T* p, float (&v)[8]) {
+  if (p) {
+    load8(p, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+  }
+}
+
+// Taps of 8 channels ([c][4] in memory) by tap, and their bias.
+template <typename T>
+__device__ __forceinline__ void load_taps(const SsmArgs& a, int c, float (&w)[4][8],
+                                          float (&b)[8]) {
+  const T* p = static_cast<const T*>(a.conv_w) + (size_t)c * 4;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float v[8];
+    load8(p + 8 * q, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e & 3][2 * q + (e >> 2)] = v[e];
+  }
+  load8_or_zero(a.conv_b ? static_cast<const T*>(a.conv_b) + c : nullptr, b);
+}
+
+// Final conv history of sequence n (tokens [s, end), pool row `row`): the last three rows of its
+// history followed by its tokens.  Block k of the sequence's nb blocks takes its share of the
+// channels; a thread reads its 8 channels before it writes them, so convN may be conv0 (the conv,
+// which reads conv0 too, has finished).
+template <typename T>
+__device__ __forceinline__ void conv_history(const SsmArgs& a, int n, int row, int s, int end,
+                                             int k, int nb) {
+  if (!a.convN || row < 0) return;
+  const T* c0 = static_cast<const T*>(a.conv0);
+  for (int c = (k * (int)blockDim.x + (int)threadIdx.x) * 8; c < a.Cc;
+       c += nb * (int)blockDim.x * 8) {
+    float r[3][8];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const int t = end - 3 + j;  // may lie before the sequence
+      load8_or_zero(t >= s ? static_cast<const T*>(a.x) + (size_t)t * a.Cc + c
+                           : (c0 ? c0 + ((size_t)row * 3 + 3 + t - s) * a.Cc + c : nullptr),
+                    r[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      store8(static_cast<T*>(a.convN) + ((size_t)row * 3 + j) * a.Cc + c, r[j]);
+  }
+}
+
+// Arguments of the tensor-core prefill (ssm_tc.cu).  Per chunk of 128 tokens and group:
+struct SsmTcArgs {
+  SsmArgs a;
+  uint8_t* tiles;        // C (fp16), B high, B low (bf16): [128][128] each, as swizzled row tiles
+  __half* cb;            // [128][128] C B^T, blocks of 32 columns up to the diagonal
+  int8_t* ex;            // [2][128] exponents of the rows of B and of C
+  __nv_bfloat16* hist;   // [N][3][Cc] initial conv history (NULL: zeros)
+  float* seg_state;      // [segments][H][P][NS] state added by each segment
+  double* seg_decay;     // [segments][H] log2 of its decay
+  uint64_t wait_ns;
+  int NS, seg;           // state width; chunks per segment
+};
+
+}  // namespace gdn

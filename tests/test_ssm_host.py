@@ -29,6 +29,7 @@ def test_shapes(L):
     assert L.gdn_ssm_conv_channels(None) == -1
     f = L.gdn_ssm_prefill_workspace_size
     assert 0 < f(ref(), 1, 1, 100) < f(ref(), 1, 1, 1000)
+    assert f(ref(), 1, 0, 0) > 0 and f(ref(), 0, 0, 0) > 0
     assert f(None, 1, 1, 100) == 0 and f(ref(), 1, -1, 5) == 0 and f(ref(), 4, 1, 5) == 0
     assert f(ref(head_dim=96), 1, 1, 100) == 0
     assert L.gdn_ssm_decode_workspace_size(ref(), -1) == 0
