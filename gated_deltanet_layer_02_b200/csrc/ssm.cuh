@@ -82,10 +82,13 @@ __device__ __forceinline__ void conv_history(const SsmArgs& a, int n, int row, i
 // Arguments of the tensor-core prefill (ssm_tc.cu).  Per chunk of 128 tokens and group:
 struct SsmTcArgs {
   SsmArgs a;
-  uint8_t* tiles;        // C (fp16), B high, B low (bf16): [128][128] each, as swizzled row tiles
+  uint8_t* tiles;        // C, B high, B low (fp16): [128][128] each, as swizzled row tiles
   __half* cb;            // [128][128] C B^T, blocks of 32 columns up to the diagonal
   int8_t* ex;            // [2][128] exponents of the rows of B and of C
   __nv_bfloat16* hist;   // [N][3][Cc] initial conv history (NULL: zeros)
+  float* gate;           // per chunk and head: [3][128] w, log2(delta) - cum, cum (see gates)
+  float* block;          // per chunk and head: [4] log2 decays of the blocks of 32 tokens
+  double* decay;         // per chunk and head: log2 of its decay
   float* seg_state;      // [segments][H][P][NS] state added by each segment
   double* seg_decay;     // [segments][H] log2 of its decay
   uint64_t wait_ns;

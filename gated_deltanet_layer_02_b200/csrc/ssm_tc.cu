@@ -3,21 +3,23 @@
 //
 // With cum_i the running log2 of the decay inside a chunk, delta the steps, u the conv outputs:
 //   Y    = diag(2^cum) C S^T + P X,   P_ij = 2^(cum_i - cum_j) delta_j C_i.B_j  (j <= i)
-//   S^T <- 2^cum_L S^T + B^T diag(2^(cum_L - cum_j) delta_j) X
-// Precision.  The state is returned in fp32, so its update keeps both factors in two bf16 parts
-// (three products, 2^-16 of each factor is left out); outputs are rounded to bf16, so their
-// products take fp16 operands (11 bits) once.  fp16 has few exponent bits: rows of C, B and X are
-// scaled by a power of two each (exponent from the row's largest value), S by one per chunk, and
-// P by the row's largest weight, so that nothing overflows and what underflows is 2^-24 of what
-// it is added to.  With lf_j = log2(delta_j) + the exponents of rows X_j and B_j,
-//   g_j = lf_j - cum_j,  pm_i = max over j <= i of g_j:   P^_ij = (C^_i.B^_j) 2^(g_j - pm_i)
+//   S^T <- 2^cum_L S^T + B^T diag(w) X,   w_j = 2^(cum_L - cum_j) delta_j
+// Precision.  All products take fp16 operands (11 bits) and sum in fp32.  Outputs are rounded to
+// bf16, so their operands are rounded to fp16 once.  The state is returned in fp32, so its update
+// keeps both factors in two fp16 parts (three products; what is left out is 2^-22 of them).  fp16
+// has few exponent bits: rows of C, B and X are scaled by a power of two each (exponent from the
+// row's largest value), S and wX by one per chunk, and P by the row's largest weight.  Nothing
+// overflows then, and what underflows is 2^-24 of what it is added to.  With the exponents eX, eB of
+// rows of X and B: g_j = log2(delta_j) - cum_j + eX_j + eB_j, pm_i = max over j <= i of g_j,
+//   P^_ij = (C^_i.B^_j) 2^(g_j - pm_i)
 // (never above the product), and row i of the result counts 2^(cum_i + pm_i + exponent of C_i).
-// cum and g are kept in fp64 (they reach thousands, and only their differences count).
+// A NaN or infinity in x reaches outputs of its whole chunk (zero weights do not remove it).
 //
 // Kernels (programmatic dependent launch between them):
-//   bc    per (chunk, group): conv of B and C; the operand tiles C^ (fp16) and B (two bf16
-//         parts) in the swizzled layout the products read, C^ B^^T (tcgen05) as fp16; and a copy
-//         of the initial conv history, so that the final one may overwrite it.
+//   bc    per (chunk, group): conv of B and C; the operand tiles C^ and B (two parts) in the
+//         swizzled layout the products read, and C^ B^^T (tcgen05) as fp16.  Further CTAs per
+//         (chunk, 32 heads): steps, decays (summed in fp64) and weights of the chunk's tokens.
+//         The initial conv history is copied, so that the final one may overwrite it.
 //   seg   per (segment of a sequence that another one follows, 128 channels): the state it adds.
 //   main  per (segment, 128 channels): the state that enters it (from the segments before), then
 //         chunk by chunk the outputs and the state.
@@ -44,15 +46,55 @@ constexpr int kPipe = 256;                 // threads of one 64-channel pipeline
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major) {
   return idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
-
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                       uint32_t idesc, uint32_t accumulate) {
+// tcgen05.mma issued by the lane with `lead` of a whole warp that runs this code together (the
+// descriptors stay in uniform registers: 40 products issue in 0.3 us instead of 2.3 us from a
+// single diverged thread).  mma_ss: both operands in shared memory; mma_ts: A in TMEM (row i in
+// lane i, two fp16 per 32-bit column).
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t adesc,
+                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem,
+                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+// Arrive at named barrier `id` of n threads without waiting.
+__device__ __forceinline__ void bar_arrive_n(int id, int n) {
+  asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+// Shared memory by 32-bit address.
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
@@ -61,35 +103,68 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
       : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
+// One instruction each; results below 2^-126 are zero.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float2 v) {
+  const __half2 h = __floats2half2_rn(v.x, v.y);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
-// v = high part + low part, both bf16 (half a step each)
-__device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(v.x, v.y);
-  const float2 h = unpack_bf16x2(hi);
-  lo = pack_bf16x2(v.x - h.x, v.y - h.y);
+__device__ __forceinline__ float2 mul2(float2 v, float s) {
+  return __fmul2_rn(v, make_float2(s, s));
 }
-// silu by one exponential and one division, each good to about 2^-22
-__device__ __forceinline__ float silu_div(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
+// v = high part + low part, both fp16 (half a step each)
+__device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
+  hi = pack_f16x2(v);
+  const float2 h = unpack_f16x2(hi);
+  lo = pack_f16x2(__ffma2_rn(h, make_float2(-1.f, -1.f), v));
+}
+// silu of two values with three special-function results instead of four: the two divisors
+// 1 + e^-x share one reciprocal.  The exponent is bounded so that their product stays finite;
+// below -43 sigmoid counts as e^-43.
+__device__ __forceinline__ float2 silu2(float2 x) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float2 v = mul2(make_float2(fmaxf(x.x, -43.f), fmaxf(x.y, -43.f)), -kLog2e);
+  const float2 d = __fadd2_rn(make_float2(ex2(v.x), ex2(v.y)), make_float2(1.f, 1.f));
+  return __fmul2_rn(x, mul2(make_float2(d.y, d.x), rcp(d.x * d.y)));
+}
 
 // Exponent of the largest magnitude of a row (its bits), within [-100, 127]; the row is scaled
 // by pow2(target - exponent).
-__device__ __forceinline__ int exponent_of(uint32_t abs_bits) {
-  return max((int)(abs_bits >> 23) - 127, -100);
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ int exponent_of(uint32_t bits) {
+  return max((int)(bits >> 23) - 127, -100);
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
-constexpr int kTargetBC = 3;   // rows of C and B below 2^4: their products stay below 2^15
+// v 2^e for any e a call can form
+__device__ __forceinline__ float scale2(float v, int e) {
+  const int h = max(min(e, 250), -250) >> 1;
+  return v * pow2(h) * pow2(max(min(e, 250), -250) - h);
+}
+constexpr int kTargetC = 3;    // C below 2^4
+constexpr int kTargetB = 13;   // B below 2^14: C B^T below 2^25, kept as fp16 scaled by 2^-10
+constexpr int kScaleCB = -10;
 constexpr int kTargetX = 13;
 constexpr int kTargetS = 14;
+constexpr int kTargetW = 12;   // wX below 2^14 (two factors, each below 2 of its exponent)
 
 // Unit k of the packed batch: sequences cut into units of `tokens`, numbered sequence by
-// sequence; with `empty` a sequence without tokens has one unit too.  All threads of the CTA
-// call it; scratch: 3 int64 per warp and a Unit in shared memory.
+// sequence; with `empty` a sequence without tokens has one unit too.  Every warp finds it by
+// itself, 128 sequences at a time (4 per lane).  `most_units`: units the launch has room for.
 struct Unit {
   int n;        // sequence, or -1: no such unit
   int j;        // unit inside the sequence
@@ -97,68 +172,142 @@ struct Unit {
   int chunk;    // first chunk of the sequence
   int first;    // first unit of the sequence
 };
-// `most_units`: units the launch has room for.
 __device__ __forceinline__ Unit find_unit(const SsmArgs& a, int tokens, bool empty, int k,
-                                          int64_t most_units, void* scratch) {
-  int64_t* wsum = reinterpret_cast<int64_t*>(scratch);  // [warps][2]
-  Unit* res = reinterpret_cast<Unit*>(wsum + 64);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+                                          int most_units) {
+  const int lane = threadIdx.x & 31;
   const int64_t most = (int64_t)a.T / kL + a.N;  // chunks the workspace holds
-  if (tid == 0) res->n = -1;
+  Unit r{-1, 0, 0, 0, 0, 0};
   int64_t u0 = 0, c0 = 0;
-  for (int base = 0; base < a.N; base += blockDim.x) {
-    const int n = base + tid;
-    int s = 0, e = 0;
-    if (n < a.N) seq_range(a, n, s, e);
-    const int nc = (e - s + kL - 1) / kL;
-    const int nu = n < a.N ? max((e - s + tokens - 1) / tokens, empty ? 1 : 0) : 0;
-    int64_t ui = nu, ci = nc;
+  for (int base = 0; base < a.N && u0 <= k; base += 128) {
+    int s[4], e[4];
+    uint32_t nu[4], nc[4], us = 0, cs = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = base + 4 * lane + q;
+      s[q] = e[q] = 0;
+      if (n < a.N) seq_range(a, n, s[q], e[q]);
+      nc[q] = (uint32_t)(e[q] - s[q] + kL - 1) / kL;
+      nu[q] = n < a.N ? max((uint32_t)(e[q] - s[q] + tokens - 1) / (uint32_t)tokens, empty ? 1u : 0u)
+                      : 0u;
+      us += nu[q];
+      cs += nc[q];
+    }
+    uint32_t ui = us, ci = cs;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t uu = __shfl_up_sync(0xffffffffu, ui, o);
-      const int64_t cc = __shfl_up_sync(0xffffffffu, ci, o);
+      const uint32_t uu = __shfl_up_sync(0xffffffffu, ui, o);
+      const uint32_t cc = __shfl_up_sync(0xffffffffu, ci, o);
       if (lane >= o) {
         ui += uu;
         ci += cc;
       }
     }
-    __syncthreads();
-    if (lane == 31) {
-      wsum[2 * warp] = ui;
-      wsum[2 * warp + 1] = ci;
-    }
-    __syncthreads();
-    int64_t ub = u0, cb = c0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) {
-        ub += wsum[2 * w];
-        cb += wsum[2 * w + 1];
+    int64_t uf = u0 + ui - us, cf = c0 + ci - cs;
+    bool mine = false;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (k >= uf && k < uf + nu[q]) {
+        mine = true;
+        r = Unit{base + 4 * lane + q, (int)(k - uf), s[q], e[q], (int)cf, (int)uf};
+        if (cf + nc[q] > most || uf + nu[q] > most_units) {
+          // sequences that overlap: no room for this one, it counts as empty
+          report_status(a.status, GDN_ERR_INVALID_ARG);
+          r.e = r.s;
+          if (r.j > 0 || !empty) r.n = -1;
+        }
       }
-      u0 += wsum[2 * w];
-      c0 += wsum[2 * w + 1];
+      uf += nu[q];
+      cf += nc[q];
     }
-    const int64_t uf = ub + ui - nu, cf = cb + ci - nc;
-    if (k >= uf && k < uf + nu) {
-      Unit r{n, (int)(k - uf), s, e, (int)cf, (int)uf};
-      if (cf + nc > most || uf + nu > most_units) {  // sequences that overlap: no room for it
-        report_status(a.status, GDN_ERR_INVALID_ARG);
-        r.e = r.s;
-        if (r.j > 0 || !empty) r.n = -1;
-      }
-      *res = r;
+    const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    if (who) {
+      const int l = __ffs(who) - 1;
+      r.n = __shfl_sync(0xffffffffu, r.n, l);
+      r.j = __shfl_sync(0xffffffffu, r.j, l);
+      r.s = __shfl_sync(0xffffffffu, r.s, l);
+      r.e = __shfl_sync(0xffffffffu, r.e, l);
+      r.chunk = __shfl_sync(0xffffffffu, r.chunk, l);
+      r.first = __shfl_sync(0xffffffffu, r.first, l);
+      return r;
     }
-    if (u0 > k) break;  // uniform: every thread adds the same sums
+    u0 += __shfl_sync(0xffffffffu, ui, 31);
+    c0 += __shfl_sync(0xffffffffu, ci, 31);
   }
-  __syncthreads();
-  const Unit r = *res;
-  __syncthreads();
   return r;
 }
 
 // ------------------------------------------------------------------------------------- bc
-// 256 threads: lanes 0-15 hold 8 channels of B each, lanes 16-31 of C; warp w has tokens
-// 16 w .. 16 w + 15 of the chunk.  State widths below 128 are padded with zero channels.
+// 256 threads: warp w has tokens 16 w .. 16 w + 15 of the chunk, first of B, then of C; a lane
+// holds 4 channels of a row.  State widths below 128 are padded with zero channels.
 constexpr uint32_t kBcSmem = 4 * kTileB + 2048;
+constexpr int kGateHeads = 32;  // heads per gates CTA
+
+// Steps, decays and weights of the chunk's tokens for 32 heads.  Rows of [chunk][H][3][128]: w,
+// log2(delta) - cum, cum, the latter two with cum counted from the start of the token's block of
+// 32; the log2 decay of each block; and that of the chunk in fp64.  The sums run in fp64: cum may
+// reach thousands while only its differences count, to 2^-22 in w.
+__device__ __forceinline__ void gates(const SsmTcArgs& g, const Unit& un, int part, float* d_s) {
+  const SsmArgs& a = g.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int t0 = un.s + un.j * kL, L = min(kL, un.e - t0), h0 = part * kGateHeads;
+  {
+    const int h = h0 + lane;
+    const float bias = h < a.H && a.dt_bias ? a.dt_bias[h] : 0.f;
+    float raw[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int i = warp + 8 * q;
+      raw[q] = h < a.H && i < L ? __ldg(a.dt + (size_t)(t0 + i) * a.H + h) : 0.f;
+    }
+#pragma unroll 4
+    for (int q = 0; q < 16; ++q) {
+      const int i = warp + 8 * q;
+      d_s[lane * 132 + i] = h < a.H && i < L ? ssm_step(raw[q] + bias, a.dt_min, a.dt_max) : 0.f;
+    }
+  }
+  __syncthreads();
+  for (int hh = warp; hh < kGateHeads; hh += 8) {
+    const int h = h0 + hh;
+    if (h >= a.H) break;
+    const float rate2 = -1.4426950408889634f * expf(a.a_log[h]);
+    const float4 d4 = *reinterpret_cast<const float4*>(d_s + hh * 132 + 4 * lane);
+    const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+    double c[4], sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // a decay below 2^-150 counts as 2^-150 (zero in fp32)
+      sum += (double)fmaxf(rate2 * d[e], -150.f);
+      c[e] = sum;
+    }
+    double inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    const double all = __shfl_sync(0xffffffffu, inc, 31), before = inc - sum;
+    const double start = __shfl_sync(0xffffffffu, before, lane & 24);  // of the block of 32 tokens
+    const double stop = __shfl_sync(0xffffffffu, inc, lane | 7);
+    float4 w, lf, cum;
+    float* pw = &w.x;
+    float* pl = &lf.x;
+    float* pc = &cum.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const double ce = before + c[e];
+      pw[e] = d[e] * exp2f((float)(all - ce));
+      pl[e] = (float)((double)fmaxf(log2f(d[e]), -1000.f) - (ce - start));
+      pc[e] = (float)(ce - start);
+    }
+    const size_t at = (size_t)(un.chunk + un.j) * a.H + h;
+    float4* out = reinterpret_cast<float4*>(g.gate + at * 3 * kL) + lane;
+    out[0] = w;
+    out[32] = lf;
+    out[64] = cum;
+    if (lane == 0) g.decay[at] = all;
+    if ((lane & 7) == 0) g.block[at * 4 + (lane >> 3)] = (float)(stop - start);
+  }
+}
 
 __global__ void __launch_bounds__(256, 2) ssm_bc_kernel(SsmTcArgs g) {
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -168,9 +317,14 @@ __global__ void __launch_bounds__(256, 2) ssm_bc_kernel(SsmTcArgs g) {
   uint64_t* bar = reinterpret_cast<uint64_t*>(ctl);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(ctl + 8);
   pdl_trigger();
-  const int grp = blockIdx.x % a.G;
-  const Unit un = find_unit(a, kL, false, blockIdx.x / a.G, gridDim.x / a.G, sm);
+  const int roles = a.G + (a.H + kGateHeads - 1) / kGateHeads;
+  const int grp = blockIdx.x % roles;
+  const Unit un = find_unit(a, kL, false, blockIdx.x / roles, gridDim.x / roles);
   if (un.n < 0) return;
+  if (grp >= a.G) {
+    gates(g, un, grp - a.G, reinterpret_cast<float*>(sm));
+    return;
+  }
   if (tid == 0) {
     mbar_init(bar, 1);
     fence_barrier_init();
@@ -178,10 +332,6 @@ __global__ void __launch_bounds__(256, 2) ssm_bc_kernel(SsmTcArgs g) {
   if (warp == 0) tmem_alloc(tslot, 128);
   const int t0 = un.s + un.j * kL, L = min(kL, un.e - t0);
   const size_t at = (size_t)(un.chunk + un.j) * a.G + grp;  // tile block
-  const int part = lane >> 4, vec = lane & 15;              // 0: B, 1: C
-  const bool live = vec * 8 < g.NS;
-  const int c = a.H * a.P + (part * a.G + grp) * g.NS + vec * 8;
-  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + c;
   const __nv_bfloat16* c0 = static_cast<const __nv_bfloat16*>(a.conv0);
   const int row = state_row(a.slot, un.n, a.num_slots);
   // the history the later kernels read: this group's share of the channels
@@ -193,62 +343,70 @@ __global__ void __launch_bounds__(256, 2) ssm_bc_kernel(SsmTcArgs g) {
       reinterpret_cast<uint4*>(g.hist + (size_t)un.n * 3 * a.Cc)[v] = r;
     }
   }
-  float w[4][8], b[8], h[3][8];
-  if (live) load_taps<__nv_bfloat16>(a, c, w, b);
   const int i0 = warp * 16;
-#pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    const int t = t0 + i0 - 3 + j;
-    const __nv_bfloat16* p = nullptr;
-    if (live && i0 < L) {
-      if (t >= un.s) p = x + (size_t)t * a.Cc;
-      else if (c0 && row >= 0) p = c0 + ((size_t)row * 3 + 3 + t - un.s) * a.Cc + c;
-    }
-    load8_or_zero(p, h[j]);
-  }
   uint8_t* tiles = g.tiles + at * kBcBytes;
   int8_t* ex = g.ex + at * 2 * kL;
-  for (int q = 0; q < 16; ++q) {
-    const int i = i0 + q;
-    float v[8];
-    const bool in = live && i < L;
-    load8_or_zero(in ? x + (size_t)(t0 + i) * a.Cc : nullptr, v);
-    float u[8];
-    uint32_t top = 0;
+  const bool live = lane * 4 < g.NS;
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {  // B, then C
+    const int c = a.H * a.P + (part * a.G + grp) * g.NS + lane * 4;
+    float2 w[4][2], b[2];  // taps and bias of the channel pairs
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float s = 0.f;
-      if (in)
-        s = silu_div(fmaf(w[3][e], v[e],
-                          fmaf(w[2][e], h[2][e], fmaf(w[1][e], h[1][e], fmaf(w[0][e], h[0][e], b[e])))));
-      u[e] = s;
-      top = max(top, __float_as_uint(s) & 0x7fffffffu);
-      h[0][e] = h[1][e];
-      h[1][e] = h[2][e];
-      h[2][e] = v[e];
+    for (int p = 0; p < 2; ++p) {
+      uint4 r = make_uint4(0, 0, 0, 0);
+      uint32_t rb = 0;
+      if (live) {
+        r = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.conv_w) +
+                                                 (size_t)(c + 2 * p) * 4));
+        if (a.conv_b)
+          rb = __ldg(reinterpret_cast<const uint32_t*>(
+              static_cast<const __nv_bfloat16*>(a.conv_b) + c + 2 * p));
+      }
+      const float2 wa = unpack_bf16x2(r.x), wb = unpack_bf16x2(r.y);
+      const float2 wc = unpack_bf16x2(r.z), wd = unpack_bf16x2(r.w);
+      w[0][p] = make_float2(wa.x, wc.x), w[1][p] = make_float2(wa.y, wc.y);
+      w[2][p] = make_float2(wb.x, wd.x), w[3][p] = make_float2(wb.y, wd.y);
+      b[p] = unpack_bf16x2(rb);
+    }
+    uint2 raw[19];
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + c;
+#pragma unroll
+    for (int q = 0; q < 19; ++q) {
+      const int t = t0 + i0 + q - 3;
+      raw[q] = make_uint2(0, 0);
+      if (live && i0 < L && i0 + q - 3 < L) {
+        if (t >= un.s)
+          raw[q] = __ldg(reinterpret_cast<const uint2*>(x + (size_t)t * a.Cc));
+        else if (c0 && row >= 0)
+          raw[q] = *reinterpret_cast<const uint2*>(c0 + ((size_t)row * 3 + 3 + t - un.s) * a.Cc + c);
+      }
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e2 = exponent_of(top);
-    const float sc = pow2(kTargetBC - e2);
-    if (vec == 0) ex[part * kL + i] = (int8_t)e2;
-    uint4 f;
-    f.x = pack_f16x2(u[0] * sc, u[1] * sc);
-    f.y = pack_f16x2(u[2] * sc, u[3] * sc);
-    f.z = pack_f16x2(u[4] * sc, u[5] * sc);
-    f.w = pack_f16x2(u[6] * sc, u[7] * sc);
-    const uint32_t off = (vec >> 3) * kTileB + sw128_off(i, vec & 7);
-    *reinterpret_cast<uint4*>(sm + part * 2 * kTileB + off) = f;
-    if (part) {
-      *reinterpret_cast<uint4*>(tiles + off) = f;
-    } else {
-      uint4 hi, lo;
-      split2(make_float2(u[0], u[1]), hi.x, lo.x);
-      split2(make_float2(u[2], u[3]), hi.y, lo.y);
-      split2(make_float2(u[4], u[5]), hi.z, lo.z);
-      split2(make_float2(u[6], u[7]), hi.w, lo.w);
-      *reinterpret_cast<uint4*>(tiles + 2 * kTileB + off) = hi;
-      *reinterpret_cast<uint4*>(tiles + 4 * kTileB + off) = lo;
+    for (int q = 0; q < 16; ++q) {
+      const int i = i0 + q;
+      float2 u[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        auto word = [&](const uint2& r) { return unpack_bf16x2(p ? r.y : r.x); };
+        float2 y = __ffma2_rn(w[0][p], word(raw[q]), b[p]);
+        y = __ffma2_rn(w[1][p], word(raw[q + 1]), y);
+        y = __ffma2_rn(w[2][p], word(raw[q + 2]), y);
+        u[p] = silu2(__ffma2_rn(w[3][p], word(raw[q + 3]), y));
+        if (i >= L) u[p] = make_float2(0.f, 0.f);
+      }
+      const uint32_t top = __reduce_max_sync(
+          0xffffffffu, max(max(abs_bits(u[0].x), abs_bits(u[0].y)),
+                           max(abs_bits(u[1].x), abs_bits(u[1].y))));
+      const int e2 = exponent_of(top);
+      if (lane == 0) ex[part * kL + i] = (int8_t)e2;
+      const float sc = pow2((part ? kTargetC : kTargetB) - e2);
+      uint2 hi, lo;
+      split2(mul2(u[0], sc), hi.x, lo.x);
+      split2(mul2(u[1], sc), hi.y, lo.y);
+      const uint32_t off = (lane >> 4) * kTileB + sw128_off(i, (lane & 15) >> 1) + (lane & 1) * 8;
+      *reinterpret_cast<uint2*>(sm + part * 2 * kTileB + off) = hi;
+      *reinterpret_cast<uint2*>(tiles + (part ? 0 : 2 * kTileB) + off) = hi;
+      if (!part) *reinterpret_cast<uint2*>(tiles + 4 * kTileB + off) = lo;
     }
   }
   fence_proxy_async_smem();
@@ -277,10 +435,10 @@ __global__ void __launch_bounds__(256, 2) ssm_bc_kernel(SsmTcArgs g) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint4 f;
-      f.x = pack_f16x2(v[8 * q], v[8 * q + 1]);
-      f.y = pack_f16x2(v[8 * q + 2], v[8 * q + 3]);
-      f.z = pack_f16x2(v[8 * q + 4], v[8 * q + 5]);
-      f.w = pack_f16x2(v[8 * q + 6], v[8 * q + 7]);
+      f.x = pack_f16x2(mul2(make_float2(v[8 * q], v[8 * q + 1]), pow2(kScaleCB)));
+      f.y = pack_f16x2(mul2(make_float2(v[8 * q + 2], v[8 * q + 3]), pow2(kScaleCB)));
+      f.z = pack_f16x2(mul2(make_float2(v[8 * q + 4], v[8 * q + 5]), pow2(kScaleCB)));
+      f.w = pack_f16x2(mul2(make_float2(v[8 * q + 6], v[8 * q + 7]), pow2(kScaleCB)));
       *reinterpret_cast<uint4*>(cb + blk * 32 + 8 * q) = f;
     }
   }
@@ -297,8 +455,6 @@ __global__ void __launch_bounds__(256, 2) ssm_bc_kernel(SsmTcArgs g) {
 struct Slice {
   bool live;
   int h, c;        // head; first channel (of x and of the output)
-  float rate2;     // log2(e) exp(a_log)
-  float bias;
 };
 __device__ __forceinline__ Slice slice_of(const SsmTcArgs& g, int grp, int v, int slices) {
   const SsmArgs& a = g.a;
@@ -307,114 +463,146 @@ __device__ __forceinline__ Slice slice_of(const SsmTcArgs& g, int grp, int v, in
   const int blocks = a.P / 64;
   s.h = grp * (a.H / a.G) + (s.live ? v / blocks : 0);
   s.c = s.h * a.P + (s.live ? v % blocks : 0) * 64;
-  s.rate2 = -1.4426950408889634f * expf(a.a_log[s.h]);
-  s.bias = a.dt_bias ? a.dt_bias[s.h] : 0.f;
   return s;
-}
-
-__device__ __forceinline__ float load_dt(const SsmArgs& a, const Slice& s, int t0, int L, int i) {
-  return i < L ? __ldg(a.dt + (size_t)(t0 + i) * a.H + s.h) : 0.f;
-}
-// Step of a token (0 behind the chunk's end) and log2 of its decay.  A decay below 2^-150 counts
-// as 2^-150 (zero in fp32).
-__device__ __forceinline__ float chunk_step(const SsmArgs& a, const Slice& s, float raw, bool in,
-                                            double& la) {
-  const float d = in ? ssm_step(raw + s.bias, a.dt_min, a.dt_max) : 0.f;
-  la = (double)fmaxf(s.rate2 * d, -150.f);
-  return d;
 }
 // 128 bytes towards L2, for the next chunk
 __device__ __forceinline__ void prefetch_row(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
-__device__ __forceinline__ double warp_scan_add(double v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+
+// The rows of a chunk's 64 channels come to shared memory as 128 bulk copies of 128 bytes, one per
+// thread of the pipeline's first four warps (the barrier counts 128 arrivals); the three rows
+// before the chunk, which only the first warp needs, to its registers.
+__device__ __forceinline__ void load_x(const SsmTcArgs& g, const Unit& un, const Slice& s, int t0,
+                                       int pt, uint8_t* dst, uint64_t* bar, uint32_t (&halo)[3]) {
+  const SsmArgs& a = g.a;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + s.c;
+  if (pt < 128) {
+    const bool in = t0 + pt < un.e;
+    mbar_arrive_expect_tx(bar, in ? 128 : 0);
+    if (in) bulk_load(dst + pt * 128, x + (size_t)(t0 + pt) * a.Cc, 128, bar);
   }
-  return v;
-}
-__device__ __forceinline__ double warp_scan_max(double v, int lane) {
+  if (pt < 32) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v = fmax(v, u);
+    for (int q = 0; q < 3; ++q) {
+      const int t = t0 - 3 + q;
+      halo[q] = 0;
+      if (t >= un.s)
+        halo[q] = __ldg(reinterpret_cast<const uint32_t*>(x + (size_t)t * a.Cc) + pt);
+      else if (g.hist)
+        halo[q] = *(reinterpret_cast<const uint32_t*>(
+                        g.hist + ((size_t)un.n * 3 + 3 + t - un.s) * a.Cc + s.c) + pt);
+    }
   }
-  return v;
 }
 
-// Conv + SiLU of a chunk's 64 channels.  Lane l has channels c + 2 l, c + 2 l + 1; warp w tokens
-// 16 w .. 16 w + 15, walked with the three rows before them in registers; `put` gets token and
-// value (zero behind the chunk's end).
-template <typename Put>
-__device__ __forceinline__ void conv_x(const SsmTcArgs& g, const Unit& un, const Slice& s, int t0,
-                                       int L, int warp, int lane, Put&& put) {
+// Conv + SiLU of 64 channels of the warp's 16 tokens (16 w ..), lane l with channels c + 2 l and
+// c + 2 l + 1: u (zero behind the chunk's end) and the exponents of the token rows into ex_s.
+// `raw`: address of the chunk's rows.
+__device__ __forceinline__ void conv_x(const SsmTcArgs& g, const Slice& s, int L, int warp, int lane,
+                                       uint32_t raw, const uint32_t (&halo)[3], float2 (&u)[16],
+                                       int8_t* ex_s) {
   const SsmArgs& a = g.a;
   const int c = s.c + 2 * lane, i0 = warp * 16;
-  const uint32_t* x = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.x) + c);
-  const size_t pitch = (size_t)a.Cc / 2;
-  const uint4 wr = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.conv_w) +
-                                                   (size_t)c * 4);
+  const uint4 wr = __ldg(reinterpret_cast<const uint4*>(
+      static_cast<const __nv_bfloat16*>(a.conv_w) + (size_t)c * 4));
   const float2 wa = unpack_bf16x2(wr.x), wb = unpack_bf16x2(wr.y);
   const float2 wc = unpack_bf16x2(wr.z), wd = unpack_bf16x2(wr.w);
   const float2 w0 = make_float2(wa.x, wc.x), w1 = make_float2(wa.y, wc.y);
   const float2 w2 = make_float2(wb.x, wd.x), w3 = make_float2(wb.y, wd.y);
   float2 b = make_float2(0.f, 0.f);
   if (a.conv_b)
-    b = unpack_bf16x2(*reinterpret_cast<const uint32_t*>(
-        static_cast<const __nv_bfloat16*>(a.conv_b) + c));
-  uint32_t raw[19];
-#pragma unroll
-  for (int q = 0; q < 19; ++q) {
-    const int i = i0 + q - 3, t = t0 + i;
-    raw[q] = 0;
-    if (i < L && i0 < L) {
-      if (t >= un.s) raw[q] = __ldg(x + (size_t)t * pitch);
-      else if (g.hist)
-        raw[q] = *reinterpret_cast<const uint32_t*>(
-            g.hist + ((size_t)un.n * 3 + 3 + t - un.s) * a.Cc + c);
-    }
+    b = unpack_bf16x2(__ldg(reinterpret_cast<const uint32_t*>(
+        static_cast<const __nv_bfloat16*>(a.conv_b) + c)));
+  const uint32_t at = raw + i0 * 128 + lane * 4;
+  const int live = L - i0;  // tokens of this warp
+  float2 h0, h1, h2;
+  if (warp == 0) {
+    h0 = unpack_bf16x2(halo[0]), h1 = unpack_bf16x2(halo[1]), h2 = unpack_bf16x2(halo[2]);
+  } else {
+    h0 = unpack_bf16x2(lds32(at - 384)), h1 = unpack_bf16x2(lds32(at - 256));
+    h2 = unpack_bf16x2(lds32(at - 128));
   }
-  float2 h0 = unpack_bf16x2(raw[0]), h1 = unpack_bf16x2(raw[1]), h2 = unpack_bf16x2(raw[2]);
 #pragma unroll
   for (int q = 0; q < 16; ++q) {
-    const float2 v = unpack_bf16x2(raw[q + 3]);
-    const float2 y = __ffma2_rn(w3, v, __ffma2_rn(w2, h2, __ffma2_rn(w1, h1, __ffma2_rn(w0, h0, b))));
+    const float2 v = unpack_bf16x2(lds32(at + q * 128));
+    u[q] = silu2(__ffma2_rn(w3, v, __ffma2_rn(w2, h2, __ffma2_rn(w1, h1, __ffma2_rn(w0, h0, b)))));
     h0 = h1;
     h1 = h2;
     h2 = v;
-    float2 u = make_float2(silu_div(y.x), silu_div(y.y));
-    if (i0 + q >= L) u = make_float2(0.f, 0.f);
-    put(i0 + q, u);
+    if (q >= live) u[q] = make_float2(0.f, 0.f);
+    const float m = fmaxf(fabsf(u[q].x), fabsf(u[q].y));
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    if (lane == q) ex_s[i0 + q] = (int8_t)exponent_of(top);
   }
 }
 
-// Byte offset of the channel pair of lane l in row i of a [128][64] row tile.
-__device__ __forceinline__ uint32_t pair_off(int i, int lane) {
-  return sw128_off(i, lane >> 2) + (lane & 3) * 4;
-}
-
-// B^T wX, what a chunk adds to S^T: three products of the bf16 parts (the fourth is below 2^-16 of the first).
-__device__ __forceinline__ void mma_state(uint32_t tS, uint32_t sB, uint32_t sW) {
-  constexpr uint32_t id = idesc_bf16(128, 64, true, true);
+// B^T wX, what a chunk adds to S^T: three products of the two parts of each (the fourth is below
+// 2^-22 of the first).
+__device__ __forceinline__ void mma_state(uint32_t lead, uint32_t tS, uint32_t sB, uint32_t sW) {
+  constexpr uint32_t id = idesc_f16(128, 64, true, true);
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
     const uint32_t A = sB + (p == 1 ? 2 * kTileB : 0), W = sW + (p == 2 ? kTileB : 0);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-      mma_bf16(tS, desc_mnmajor(A, kk, kTileB), desc_mnmajor(W, kk, kTileB), id,
-               p > 0 || kk > 0);
+      mma_ss(lead, tS, desc_mnmajor(A, kk, kTileB), desc_mnmajor(W, kk, kTileB), id,
+             p > 0 || kk > 0);
+  }
+}
+
+// Exponent of the largest value row i of wX may hold (w, and the rows of X and B).
+__device__ __forceinline__ int weight_exponent(float w, int eX, int eB) {
+  return (int)(abs_bits(w) >> 23) - 127 + eX + eB;
+}
+
+// The chunk's weights, by a whole warp: lane l has tokens 4 l .. 4 l + 3.  Puts the factors of wX
+// of the warp's own tokens 16 w .. into w_s (for this warp alone: a __syncwarp orders them) and
+// returns the chunk's exponent of wX.  Every warp of the pipeline finds the same one.
+__device__ __forceinline__ int weights(const float4& w4, uint32_t ex4, uint32_t eB4, int warp,
+                                       int lane, float* w_s) {
+  const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+  int top = INT32_MIN, eB[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    eB[e] = (int)(int8_t)(eB4 >> (8 * e));
+    top = max(top, weight_exponent(w[e], (int)(int8_t)(ex4 >> (8 * e)), eB[e]));
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((lane >> 2) == warp)
+    *reinterpret_cast<float4*>(w_s + 4 * lane) =
+        make_float4(scale2(w[0], eB[0] + kTargetW - top), scale2(w[1], eB[1] + kTargetW - top),
+                    scale2(w[2], eB[2] + kTargetW - top), scale2(w[3], eB[3] + kTargetW - top));
+  __syncwarp();
+  return top;
+}
+
+// Two parts of u w of the warp's 16 tokens into the row tiles at W (high) and W + kTileB (low).
+__device__ __forceinline__ void store_wx(const float2 (&u)[16], const float* w_s, int warp, int lane,
+                                         uint32_t W) {
+  const uint32_t base = W + warp * 2048 + (lane & 3) * 4, c = (lane >> 2) << 4;
+#pragma unroll
+  for (int q = 0; q < 16; q += 4) {
+    const float4 w = *reinterpret_cast<const float4*>(w_s + warp * 16 + q);
+    const float ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t hi, lo;
+      split2(mul2(u[q + e], ws[e]), hi, lo);
+      const uint32_t at = base + (c ^ (((q + e) & 7) << 4)) + (q + e) * 128;
+      sts32(at, hi);
+      sts32(at + kTileB, lo);
+    }
   }
 }
 
 // ------------------------------------------------------------------------------------ seg
-// The state a segment adds, S_j = sum over its tokens of 2^(log decay from the token to the
+// The state a segment adds, the sum over its tokens of 2^(log decay from the token to the
 // segment's end) delta x B^T (for the first segment: and the decayed initial state), chunk by
-// chunk from its end: the decay to the end goes onto wX, the products only accumulate.
-// smem: two stages of B (64 KB), one wX (32 KB) per pipeline, control.
-constexpr uint32_t kSegW = 8 * kTileB, kSegCtl = kSegW + 4 * kTileB;
-constexpr uint32_t kSegSmem = kSegCtl + 4096;
+// chunk from its end; the chunks' contributions are added in fp32 registers.
+// smem: two stages of B (64 KB), wX (32 KB) and a chunk of x rows (16 KB) per pipeline, control.
+constexpr uint32_t kSegW = 8 * kTileB, kSegCtl = kSegW + 6 * kTileB;
+constexpr uint32_t kSegSmem = kSegCtl + 3072;
 
 __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -424,7 +612,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
   const int slices = (a.H / a.G) * (a.P / 64), pairs = (slices + 1) / 2;
   const int grp = (blockIdx.x % (a.G * pairs)) / pairs, pair = blockIdx.x % pairs;
   const Unit un = find_unit(a, g.seg * kL, true, blockIdx.x / (a.G * pairs),
-                            gridDim.x / (a.G * pairs), sm);
+                            gridDim.x / (a.G * pairs));
   pdl_wait();  // before any return: the next kernel counts on this one having waited
   if (un.n < 0) return;
   const int total = (un.e - un.s + kL - 1) / kL;  // chunks of the sequence
@@ -435,20 +623,24 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
   uint8_t* ctl = sm + kSegCtl;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctl);      // [2] B stages landed
   uint64_t* done = full + 2;                              // [2] a pipeline's products
-  int* count = reinterpret_cast<int*>(ctl + 32);          // [2] uses of a stage, both pipelines
+  uint64_t* xbar = full + 4;                              // [2] a pipeline's x rows
+  int* count = reinterpret_cast<int*>(ctl + 48);          // [2] uses of a stage, both pipelines
   int* loads = count + 2;                                 // [2] copies into it
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(ctl + 48);
-  double* tot = reinterpret_cast<double*>(ctl + 64) + pipe * 4;
-  float* w_s = reinterpret_cast<float*>(ctl + 256) + pipe * kL;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(ctl + 64);
+  float* w_s = reinterpret_cast<float*>(ctl + 128) + pipe * kL;
+  // exponents of the rows of X, of two chunks: a warp may begin the next one's conv while another
+  // has yet to read this one's
+  int8_t* ex2_s = reinterpret_cast<int8_t*>(ctl + 128 + 8 * kL) + pipe * 2 * kL;
   if (tid == 0) {
     for (int k = 0; k < 4; ++k) {
       mbar_init(full + k, 1);
       count[k] = 0;  // and loads
     }
+    mbar_init(xbar, 128);
+    mbar_init(xbar + 1, 128);
     fence_barrier_init();
   }
   if (tid < 32) tmem_alloc(tslot, 128);
-  fence_proxy_async_smem();  // find_unit's scratch is overwritten by bulk copies
   __syncthreads();
   tc_fence_after();
   const uint32_t tS = *tslot + pipe * 64;
@@ -470,9 +662,13 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
 #pragma unroll
   for (int q = 0; q < 32; ++q) v[q] = 0.f;
   double R = 0.0;  // log2 decay of the chunks behind the current one
+  float scale = 0.f;  // of the products in flight
   bool ok = true;
-  int mmas = 0;
-  uint8_t* W = sm + kSegW + pipe * 2 * kTileB;
+  int mmas = 0, xloads = 0;
+  uint8_t* W = sm + kSegW + pipe * 3 * kTileB;
+  uint8_t* raw = W + 2 * kTileB;
+  const uint32_t sB = smem_u32(sm), sW = smem_u32(W);
+  const int warp = __shfl_sync(0xffffffffu, pw, 0);  // the same for the whole warp
   // adds the products of chunk k (they have read wX and the stage then); the last pipeline
   // through with a stage fetches the next chunk but one into it
   auto take = [&](int k) {
@@ -486,59 +682,60 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
       }
     }
     __syncwarp();
-    float u[32];
-    tmem_ld32(tmem_at(tS, (pw & 3) * 32, (pw >> 2) * 32), u);
-    tmem_ld_wait();
-    tc_fence_before();
 #pragma unroll
-    for (int q = 0; q < 32; ++q) v[q] += u[q];
+    for (int r = 0; r < 2; ++r) {
+      float d[16];
+      tmem_ld16(tmem_at(tS, (pw & 3) * 32, (pw >> 2) * 32 + 16 * r), d);
+      tmem_ld_wait();
+#pragma unroll
+      for (int q = 0; q < 16; ++q) v[16 * r + q] = fmaf(scale, d[q], v[16 * r + q]);
+    }
+    tc_fence_before();
   };
   if (s.live) {
-    const int i = pt & 127;
-    float raw = load_dt(a, s, un.s + (c1 - 1) * kL, kL, i);
+    uint32_t halo[3];
+    load_x(g, un, s, un.s + (c1 - 1) * kL, pt, raw, xbar + pipe, halo);
+    xloads = 1;
     for (int k = 0; k < nch; ++k) {
-      const int t0 = un.s + (c1 - 1 - k) * kL;
-      double la;
-      const float d = chunk_step(a, s, raw, i < kL, la);
-      if (k + 1 < nch) {
-        raw = load_dt(a, s, t0 - kL, kL, i);
-        if (pt < 128) prefetch_row(static_cast<const __nv_bfloat16*>(a.x) +
-                                   (size_t)(t0 - kL + i) * a.Cc + s.c);
-      }
-      double cum = warp_scan_add(la, lane);
-      if (pt < 128 && lane == 31) tot[pw] = cum;
+      const int ch = c1 - 1 - k, t0 = un.s + ch * kL;
+      const size_t at = (size_t)(un.chunk + ch) * a.H + s.h;
+      const float4 w4 = __ldg(reinterpret_cast<const float4*>(g.gate + at * 3 * kL) + lane);
+      const uint32_t eB4 = __ldg(reinterpret_cast<const uint32_t*>(
+          g.ex + ((size_t)(un.chunk + ch) * a.G + grp) * 2 * kL) + lane);
+      const double all = __ldg(g.decay + at);
+      if (k + 2 < nch && pt < 128)
+        prefetch_row(static_cast<const __nv_bfloat16*>(a.x) + (size_t)(t0 - 2 * kL + pt) * a.Cc + s.c);
+      ok = mbar_wait(xbar + pipe, k & 1, g.wait_ns) && ok;
+      float2 u[16];
+      int8_t* ex_s = ex2_s + (k & 1) * kL;
+      conv_x(g, s, kL, warp, lane, smem_u32(raw), halo, u, ex_s);
       if (bar_or_n(1 + pipe, kPipe, !ok)) break;
-      double all = 0.0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q < (i >> 5)) cum += tot[q];
-        all += tot[q];
+      if (k + 1 < nch) {  // every warp has read its rows
+        load_x(g, un, s, t0 - kL, pt, raw, xbar + pipe, halo);
+        ++xloads;
       }
-      if (pt < 128) w_s[i] = d * exp2f((float)(R + all - cum));
-      R += all;
+      const int top = weights(w4, reinterpret_cast<const uint32_t*>(ex_s)[lane], eB4, warp, lane, w_s);
       if (k > 0) take(k - 1);
-      bar_sync_n(1 + pipe, kPipe);
-      conv_x(g, un, s, t0, kL, pw, lane, [&](int q, float2 u) {
-        const float wq = w_s[q];
-        uint32_t hi, lo;
-        split2(make_float2(u.x * wq, u.y * wq), hi, lo);
-        const uint32_t off = pair_off(q, lane);
-        *reinterpret_cast<uint32_t*>(W + off) = hi;
-        *reinterpret_cast<uint32_t*>(W + kTileB + off) = lo;
-      });
+      scale = scale2(exp2f((float)R), top - kTargetW - kTargetB);
+      R += all;
+      store_wx(u, w_s, warp, lane, sW);
       fence_proxy_async_smem();
-      bar_sync_n(1 + pipe, kPipe);
-      if (pt == 0) {
+      if (warp != 0) {
+        bar_arrive_n(3 + pipe, kPipe);
+      } else {
+        bar_sync_n(3 + pipe, kPipe);
         const bool got = mbar_wait(full + (k & 1), (k >> 1) & 1, g.wait_ns);
         tc_fence_after();
-        if (got) {
-          mma_state(tS, smem_u32(sm + (k & 1) * 4 * kTileB), smem_u32(W));
-          mma_commit(done + pipe);
+        if (__all_sync(0xffffffffu, got)) {
+          const uint32_t lead = elect_one();
+          mma_state(lead, tS, sB + (k & 1) * 4 * kTileB, sW);
+          if (lead) mma_commit(done + pipe);
           ++mmas;
+        } else {
+          ok = false;
         }
-        ok = ok && got;
+        __syncwarp();
       }
-      __syncwarp();
     }
     if (bar_or_n(1 + pipe, kPipe, !ok)) ok = false;
     if (ok) take(nch - 1);
@@ -573,6 +770,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
     if (!ok && pt == 0) {
       report_status(a.status, GDN_ERR_TIMEOUT);
       if (mmas > 0) mbar_wait(done + pipe, (mmas - 1) & 1, g.wait_ns);
+      mbar_wait(xbar + pipe, (xloads - 1) & 1, g.wait_ns);
     }
   }
   tc_fence_before();
@@ -586,6 +784,8 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
 // ----------------------------------------------------------------------------------- main
 // smem: C^ | B high | B low (96 KB, shared by both pipelines), then per pipeline X^ | wX high |
 // wX low | S^ (64 KB), and 3 KB of control: with no more to be had, the base has to be aligned.
+// The place of S^ also takes the next chunk's x rows, from the end of the products of one chunk
+// until the conv of the next has read them.
 // TMEM, per pipeline: what the chunk adds to S^T (64 columns), C S^T and P X (128), P (64).  S^T
 // itself stays in registers (32 of a row per thread): fp32 sums there round to nearest.
 constexpr uint32_t kMainPipe = 6 * kTileB, kMainCtl = kMainPipe + 8 * kTileB;
@@ -599,7 +799,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
   const int slices = (a.H / a.G) * (a.P / 64), pairs = (slices + 1) / 2;
   const int grp = (blockIdx.x % (a.G * pairs)) / pairs, pair = blockIdx.x % pairs;
   const Unit un = find_unit(a, g.seg * kL, true, blockIdx.x / (a.G * pairs),
-                            gridDim.x / (a.G * pairs), sm);
+                            gridDim.x / (a.G * pairs));
   if (un.n < 0) {
     pdl_wait();
     return;
@@ -609,23 +809,23 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
   uint64_t* c_full = reinterpret_cast<uint64_t*>(ctl);
   uint64_t* b_full = c_full + 1;
   uint64_t* done = c_full + 2;  // [2] a pipeline's products of a chunk
-  int* count = reinterpret_cast<int*>(ctl + 32);  // chunks finished, over both pipelines
+  uint64_t* xbar = c_full + 4;  // [2] a pipeline's x rows
+  int* count = reinterpret_cast<int*>(ctl + 48);  // chunks finished, over both pipelines
   int* loads = count + 1;                         // chunks whose tiles were fetched
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(ctl + 40);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(ctl + 56);
   uint8_t* mine = ctl + 64 + pipe * 1408;
-  double* tot = reinterpret_cast<double*>(mine);           // [4] sums of la over 32 tokens
-  double* ref_s = tot + 4;                                 // [4] maxima of g over them
-  uint32_t* top_s = reinterpret_cast<uint32_t*>(mine + 64);  // [8]
-  float* wf_s = reinterpret_cast<float*>(mine + 128);      // [128] weights of wX, then F
-  float* g_s = wf_s + kL;                                  // [128]
-  int8_t* ex_s = reinterpret_cast<int8_t*>(g_s + kL);      // [128]
+  uint32_t* top_s = reinterpret_cast<uint32_t*>(mine);      // [8] largest magnitudes of S
+  float* w_s = reinterpret_cast<float*>(mine + 64);         // [128] factors of wX
+  float* f_s = w_s + kL;                                    // [128] F: 2^(g - maximum so far)
+  int8_t* ex_s = reinterpret_cast<int8_t*>(f_s + kL);       // [128] exponents of the rows of X
   if (tid == 0) {
     for (int k = 0; k < 4; ++k) mbar_init(c_full + k, 1);
+    mbar_init(xbar, 128);
+    mbar_init(xbar + 1, 128);
     *count = *loads = 0;
     fence_barrier_init();
   }
   if (tid < 32) tmem_alloc(tslot, 512);
-  fence_proxy_async_smem();  // find_unit's scratch is overwritten by bulk copies
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
@@ -657,27 +857,27 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
   float sv[32];
 #pragma unroll
   for (int q = 0; q < 32; ++q) sv[q] = 0.f;
-  {
-    if (s.live && i < g.NS) {
-      if (un.j == 0) {
-        const float* S0 = total > g.seg
-                              ? g.seg_state + (size_t)(un.first + (total - 1) / g.seg) * pitch
-                              : (a.S0 && row >= 0
-                                     ? static_cast<const float*>(a.S0) + (size_t)row * pitch
-                                     : nullptr);
-        if (S0) {
+  if (s.live && i < g.NS) {
+    if (un.j == 0) {
+      const float* S0 = total > g.seg
+                            ? g.seg_state + (size_t)(un.first + (total - 1) / g.seg) * pitch
+                            : (a.S0 && row >= 0
+                                   ? static_cast<const float*>(a.S0) + (size_t)row * pitch
+                                   : nullptr);
+      if (S0) {
 #pragma unroll
-          for (int q = 0; q < 32; ++q) sv[q] = S0[sbase + (size_t)q * g.NS];
-        }
-      } else {
-        for (int j = 0; j < un.j; ++j) {
-          const float* S = g.seg_state + (size_t)(un.first + j) * pitch + sbase;
-          const float dec = exp2f((float)g.seg_decay[(size_t)(un.first + j) * a.H + s.h]);
+        for (int q = 0; q < 32; ++q) sv[q] = S0[sbase + (size_t)q * g.NS];
+      }
+    } else {
+      for (int j = 0; j < un.j; ++j) {
+        const float* S = g.seg_state + (size_t)(un.first + j) * pitch + sbase;
+        const float dec = exp2f((float)g.seg_decay[(size_t)(un.first + j) * a.H + s.h]);
 #pragma unroll
-          for (int q = 0; q < 32; ++q) sv[q] = fmaf(dec, sv[q], S[(size_t)q * g.NS]);
-        }
+        for (int q = 0; q < 32; ++q) sv[q] = fmaf(dec, sv[q], S[(size_t)q * g.NS]);
       }
     }
+  }
+  {
     // P above the diagonal blocks is zero throughout
     float zero[32];
 #pragma unroll
@@ -686,166 +886,190 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
     tmem_st_wait();
   }
   uint8_t* X = sm + kMainPipe + pipe * 4 * kTileB;
-  uint8_t* W = X + kTileB;
-  uint8_t* S16 = X + 3 * kTileB;
+  uint8_t* raw = X + 3 * kTileB;
+  const uint32_t sC = smem_u32(sm), sX = smem_u32(X), sW = sX + kTileB, sS = sX + 3 * kTileB;
+  const int warp = __shfl_sync(0xffffffffu, pw, 0);  // the same for the whole warp
   bool ok = true;
-  int mmas = 0;
+  int mmas = 0, xloads = 0;
+  float smax = 0.f;  // largest magnitude of this thread's part of S
+#pragma unroll
+  for (int q = 0; q < 32; ++q) smax = fmaxf(smax, fabsf(sv[q]));
   if (s.live) {
-    float raw = nch > 0 ? load_dt(a, s, un.s + c0 * kL, un.e - un.s - c0 * kL, i) : 0.f;
+    uint32_t halo[3];
+    if (nch > 0) {
+      load_x(g, un, s, un.s + c0 * kL, pt, raw, xbar + pipe, halo);
+      xloads = 1;
+    }
     for (int k = 0; k < nch; ++k) {
       const int t0 = un.s + (c0 + k) * kL, L = min(kL, un.e - t0);
-      const size_t at = (size_t)(un.chunk + c0 + k) * a.G + grp;
-      // ---- steps and decays of the chunk's tokens (thread i: token i)
-      double la;
-      const float d = chunk_step(a, s, raw, i < L, la);
-      if (k + 1 < nch) {  // the next chunk's inputs on their way
-        const int t1 = t0 + kL;
-        raw = load_dt(a, s, t1, un.e - t1, i);
-        if (t1 + i < un.e) {
-          if (half == 0)
-            prefetch_row(static_cast<const __nv_bfloat16*>(a.x) + (size_t)(t1 + i) * a.Cc + s.c);
-          else if (a.z)
-            prefetch_row(static_cast<const __nv_bfloat16*>(a.z) + (size_t)(t1 + i) * a.H * a.P +
-                         s.c);
-        }
+      const size_t chunk = (size_t)(un.chunk + c0 + k), at = chunk * a.G + grp;
+      const float* gate = g.gate + (chunk * a.H + s.h) * 3 * kL;
+      const int8_t* ex = g.ex + at * 2 * kL;
+      const float4 w4 = __ldg(reinterpret_cast<const float4*>(gate) + lane);
+      const float4 lf4 = __ldg(reinterpret_cast<const float4*>(gate + kL) + lane);
+      const float lf = __ldg(gate + kL + i), cum = __ldg(gate + 2 * kL + i);
+      const float4 bt = __ldg(reinterpret_cast<const float4*>(g.block) + chunk * a.H + s.h);
+      const uint32_t eB4 = __ldg(reinterpret_cast<const uint32_t*>(ex) + lane);
+      const int eB = __ldg(ex + i), eC = __ldg(ex + kL + i);
+      if (t0 + kL + i < un.e && k + 1 < nch) {  // the next chunk's inputs on their way
+        const size_t t1 = (size_t)t0 + kL + i;
+        if (half == 0) prefetch_row(static_cast<const __nv_bfloat16*>(a.x) + t1 * a.Cc + s.c);
+        else if (a.z)
+          prefetch_row(static_cast<const __nv_bfloat16*>(a.z) + t1 * a.H * a.P + s.c);
       }
-      double cum = warp_scan_add(la, lane);
-      if (pt < 128 && lane == 31) tot[quad] = cum;
-      // ---- S^T: its largest magnitude
-      uint32_t top = 0;
-#pragma unroll
-      for (int q = 0; q < 32; ++q) top = max(top, __float_as_uint(sv[q]) & 0x7fffffffu);
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) top_s[pw] = top;
-      tc_fence_before();
+      // ---- conv of X; the largest magnitude of S
+      ok = mbar_wait(xbar + pipe, k & 1, g.wait_ns) && ok;
+      float2 u[16];
+      conv_x(g, s, L, warp, lane, sS, halo, u, ex_s);
+      uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));
+      if (lane == 0) top_s[warp] = top;
       if (bar_or_n(1 + pipe, kPipe, !ok)) break;
-      double all = 0.0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q < quad) cum += tot[q];
-        all += tot[q];
-      }
-      if (half == 0) wf_s[i] = d * exp2f((float)(all - cum));
-#pragma unroll
-      for (int q = 0; q < 8; ++q) top = max(top, top_s[q]);
-      const int eS = exponent_of(top);
       // ---- S^ = fp16 operand of C S^T
+      {
+        const uint4 ta = *reinterpret_cast<const uint4*>(top_s);
+        const uint4 tb = *reinterpret_cast<const uint4*>(top_s + 4);
+        top = max(max(max(ta.x, ta.y), max(ta.z, ta.w)), max(max(tb.x, tb.y), max(tb.z, tb.w)));
+      }
+      const int eS = exponent_of(top);
       {
         const float sc = pow2(kTargetS - eS);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint4 f;
-          f.x = pack_f16x2(sv[8 * q] * sc, sv[8 * q + 1] * sc);
-          f.y = pack_f16x2(sv[8 * q + 2] * sc, sv[8 * q + 3] * sc);
-          f.z = pack_f16x2(sv[8 * q + 4] * sc, sv[8 * q + 5] * sc);
-          f.w = pack_f16x2(sv[8 * q + 6] * sc, sv[8 * q + 7] * sc);
-          *reinterpret_cast<uint4*>(S16 + sw128_off(i, half * 4 + q)) = f;
+          f.x = pack_f16x2(mul2(make_float2(sv[8 * q], sv[8 * q + 1]), sc));
+          f.y = pack_f16x2(mul2(make_float2(sv[8 * q + 2], sv[8 * q + 3]), sc));
+          f.z = pack_f16x2(mul2(make_float2(sv[8 * q + 4], sv[8 * q + 5]), sc));
+          f.w = pack_f16x2(mul2(make_float2(sv[8 * q + 6], sv[8 * q + 7]), sc));
+          sts128(sS + sw128_off(i, half * 4 + q), f);
         }
       }
-      bar_sync_n(1 + pipe, kPipe);  // the weights
-      // ---- X^ and wX
-      conv_x(g, un, s, t0, L, pw, lane, [&](int q, float2 u) {
-        const uint32_t m = __reduce_max_sync(
-            0xffffffffu,
-            max(__float_as_uint(u.x) & 0x7fffffffu, __float_as_uint(u.y) & 0x7fffffffu));
-        const int e = exponent_of(m);
-        if (lane == 0) ex_s[q] = (int8_t)e;
-        const float sc = pow2(kTargetX - e), wq = wf_s[q];
-        uint32_t hi, lo;
-        split2(make_float2(u.x * wq, u.y * wq), hi, lo);
-        const uint32_t off = pair_off(q, lane);
-        *reinterpret_cast<uint32_t*>(X + off) = pack_f16x2(u.x * sc, u.y * sc);
-        *reinterpret_cast<uint32_t*>(W + off) = hi;
-        *reinterpret_cast<uint32_t*>(W + kTileB + off) = lo;
-      });
+      // ---- weights of wX; X^ and wX
+      const uint32_t ex4 = reinterpret_cast<const uint32_t*>(ex_s)[lane];
+      const int wt = weights(w4, ex4, eB4, warp, lane, w_s);
+      store_wx(u, w_s, warp, lane, sW);
+      {
+        const uint32_t base = sX + warp * 2048 + (lane & 3) * 4, c = (lane >> 2) << 4;
+#pragma unroll
+        for (int q = 0; q < 16; q += 4) {
+          const uint32_t e4 = *reinterpret_cast<const uint32_t*>(ex_s + warp * 16 + q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sts32(base + (c ^ (((q + e) & 7) << 4)) + (q + e) * 128,
+                  pack_f16x2(mul2(u[q + e], pow2(kTargetX - (int)(int8_t)(e4 >> (8 * e))))));
+        }
+      }
+      // ---- g of token i and its running maximum, in units of its block's start; the maxima M of
+      // the blocks (lane l: tokens 4 l ..), and what they are from this block on (ref)
+      const int eX = ex_s[i];
+      const float gi = lf + (float)(eX + eB);
+      float pm = gi;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float up = __shfl_up_sync(0xffffffffu, pm, o);
+        if (lane >= o) pm = fmaxf(pm, up);
+      }
+      float gm;
+      {
+        const float l4[4] = {lf4.x, lf4.y, lf4.z, lf4.w};
+        gm = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          gm = fmaxf(gm, l4[e] + (float)((int)(int8_t)(ex4 >> (8 * e)) + (int)(int8_t)(eB4 >> (8 * e))));
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+      }
+      const float M0 = __shfl_sync(0xffffffffu, gm, 0);
+      const float M1 = fmaxf(M0 + bt.x, __shfl_sync(0xffffffffu, gm, 8));
+      const float M2 = fmaxf(M1 + bt.y, __shfl_sync(0xffffffffu, gm, 16));
+      const float M3 = fmaxf(M2 + bt.z, __shfl_sync(0xffffffffu, gm, 24));
+      float ref[3], cs, Mq;  // cs: decay up to this block
+      if (quad == 0) {
+        cs = 0.f, Mq = M0, ref[0] = ref[1] = ref[2] = 0.f;
+      } else if (quad == 1) {
+        cs = bt.x, Mq = M1, ref[0] = M0 + bt.x, ref[1] = ref[2] = 0.f;
+        pm = fmaxf(pm, ref[0]);
+      } else if (quad == 2) {
+        cs = bt.x + bt.y, Mq = M2, ref[0] = M0 + (bt.x + bt.y), ref[1] = M1 + bt.y, ref[2] = 0.f;
+        pm = fmaxf(pm, ref[1]);
+      } else {
+        cs = bt.x + (bt.y + bt.z), Mq = M3, ref[0] = M0 + cs, ref[1] = M1 + (bt.y + bt.z);
+        ref[2] = M2 + bt.z;
+        pm = fmaxf(pm, ref[2]);
+      }
+      if (half == 0) f_s[i] = ex2(gi - Mq);
       fence_proxy_async_smem();
       tc_fence_before();
       bar_sync_n(1 + pipe, kPipe);
-      if (pt == 0) {
+      if (warp == 0) {
         const bool got = mbar_wait(c_full, k & 1, g.wait_ns) && mbar_wait(b_full, k & 1, g.wait_ns);
         tc_fence_after();
-        if (got) {
-          const uint32_t sC = smem_u32(sm), sS = smem_u32(S16);
+        if (__all_sync(0xffffffffu, got)) {
+          const uint32_t lead = elect_one();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_bf16(tI, desc_kmajor(sC, kk, kTileB), desc_mnmajor(sS, kk, kTileB),
-                     idesc_f16(128, 64, false, true), kk > 0);
-          mma_state(tS, sC + 2 * kTileB, smem_u32(W));
+            mma_ss(lead, tI, desc_kmajor(sC, kk, kTileB), desc_mnmajor(sS, kk, kTileB),
+                   idesc_f16(128, 64, false, true), kk > 0);
+          mma_state(lead, tS, sC + 2 * kTileB, sW);
+        } else {
+          ok = false;
         }
-        ok = ok && got;
+        __syncwarp();
       }
-      __syncwarp();
-      // ---- weights of P: g, its running maximum, the factors of whole blocks
-      const int8_t* ex = g.ex + at * 2 * kL;
-      const float eC = (float)__ldg(ex + kL + i);
-      const float lf = fmaxf(log2f(d), -1000.f) + (float)ex_s[i] + (float)__ldg(ex + i);
-      const double gi = (double)lf - cum;
-      double pm = warp_scan_max(gi, lane);
-      if (half == 0 && lane == 31) ref_s[quad] = pm;
-      bar_sync_n(1 + pipe, kPipe);
-      double ref[4];
-      ref[0] = ref_s[0];
-#pragma unroll
-      for (int q = 1; q < 4; ++q) ref[q] = fmax(ref[q - 1], ref_s[q]);
-      double mine_ref = ref[0];
-#pragma unroll
-      for (int q = 1; q < 4; ++q) {
-        if (q == quad) {
-          pm = fmax(pm, ref[q - 1]);
-          mine_ref = ref[q];
-        }
-      }
-      if (half == 0) {
-        g_s[i] = (float)(gi - mine_ref);
-        wf_s[i] = exp2f((float)(gi - mine_ref));
-      }
-      bar_sync_n(1 + pipe, kPipe);
-      // ---- P^ (fp16) into TMEM, block by block; this thread has 16 of each block's 32 columns
+      // ---- P^ (fp16) into TMEM: this thread has 16 columns of each block of 32 up to the diagonal
       {
         const __half* cb = g.cb + (at * kL + i) * kL + half * 16;
-        const float pmd = (float)(pm - mine_ref);
 #pragma unroll
         for (int blk = 0; blk < 4; ++blk) {
-          if (blk > quad) break;
-          const uint4 r0 = __ldg(reinterpret_cast<const uint4*>(cb + blk * 32));
-          const uint4 r1 = __ldg(reinterpret_cast<const uint4*>(cb + blk * 32 + 8));
-          const uint32_t raw[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-          uint32_t out[8];
-          const int j0 = blk * 32 + half * 16;
-          const float rf = blk < quad ? exp2f((float)(ref[blk] - pm)) : 0.f;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&raw[q]));
-            const int j = j0 + 2 * q;
-            float2 f;
+          if (blk <= quad) {
+            const uint4 r0 = __ldg(reinterpret_cast<const uint4*>(cb + blk * 32));
+            const uint4 r1 = __ldg(reinterpret_cast<const uint4*>(cb + blk * 32 + 8));
+            const uint32_t in[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+            uint32_t out[8];
+            const int j0 = blk * 32 + half * 16;
             if (blk < quad) {
-              f = *reinterpret_cast<const float2*>(wf_s + j);
-              f.x *= rf;
-              f.y *= rf;
+              const float rf = ex2(ref[blk < 3 ? blk : 2] - pm);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float4 f = *reinterpret_cast<const float4*>(f_s + j0 + 4 * q);
+                out[2 * q] = pack_f16x2(
+                    __fmul2_rn(unpack_f16x2(in[2 * q]), mul2(make_float2(f.x, f.y), rf)));
+                out[2 * q + 1] = pack_f16x2(
+                    __fmul2_rn(unpack_f16x2(in[2 * q + 1]), mul2(make_float2(f.z, f.w), rf)));
+              }
             } else {
-              const float2 e = *reinterpret_cast<const float2*>(g_s + j);
-              f.x = j <= i ? exp2f(fminf(e.x - pmd, 0.f)) : 0.f;
-              f.y = j + 1 <= i ? exp2f(fminf(e.y - pmd, 0.f)) : 0.f;
+              // the diagonal block: g of its tokens is in the lanes of this warp
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const int j = half * 16 + 2 * q;
+                const float ea = __shfl_sync(0xffffffffu, gi, j) - pm;
+                const float eb = __shfl_sync(0xffffffffu, gi, j + 1) - pm;
+                const float2 v = unpack_f16x2(in[q]);
+                out[q] = pack_f16x2(make_float2(j <= lane ? v.x * ex2(ea) : 0.f,
+                                                j + 1 <= lane ? v.y * ex2(eb) : 0.f));
+              }
             }
-            out[q] = pack_f16x2(j <= i ? v.x * f.x : 0.f, j + 1 <= i ? v.y * f.y : 0.f);
+            tmem_st8(tmem_at(tP, quad * 32, j0 / 2), out);
           }
-          tmem_st8(tmem_at(tP, quad * 32, j0 / 2), out);
         }
         tmem_st_wait();
       }
       tc_fence_before();
-      bar_sync_n(1 + pipe, kPipe);
-      if (pt == 0 && ok) {
+      if (warp != 0) {
+        bar_arrive_n(3 + pipe, kPipe);
+      } else {
+        bar_sync_n(3 + pipe, kPipe);
         tc_fence_after();
-        const uint32_t sX = smem_u32(X);
+        if (__all_sync(0xffffffffu, ok)) {
+          const uint32_t lead = elect_one();
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tX, tP + kk * 8, desc_mnmajor(sX, kk, kTileB), idesc_f16(128, 64, false, true),
-                 kk > 0);
-        mma_commit(done + pipe);
-        ++mmas;
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(lead, tX, tP + kk * 8, desc_mnmajor(sX, kk, kTileB),
+                   idesc_f16(128, 64, false, true), kk > 0);
+          if (lead) mma_commit(done + pipe);
+          ++mmas;
+        }
+        __syncwarp();
       }
-      __syncwarp();
       // ---- outputs
       const bool in = i < L;
       const size_t o_at = ((size_t)(t0 + i) * a.H) * a.P + s.c + p0;
@@ -855,6 +1079,11 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) zr[q] = __ldg(zp + q);
       }
+      const float dec = exp2f((float)__ldg(g.decay + chunk * a.H + s.h));
+      const float si = ex2(cs + cum + (float)(eC + eS - kTargetS - kTargetC));
+      const float sx = ex2((cum + pm) + (float)(eC - kTargetC - kTargetB - kScaleCB - kTargetX));
+      const float dx = D * pow2(eX - kTargetX);
+      const float ds = scale2(1.f, wt - kTargetW - kTargetB);
       ok = mbar_wait(done + pipe, k & 1, g.wait_ns) && ok;
       tc_fence_after();
       if (pt == 0 && ok) {  // the last pipeline through with the tiles fetches the next ones
@@ -865,10 +1094,12 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
         }
       }
       __syncwarp();
-      const float si = exp2f((float)cum + eC + (float)(eS - kTargetS - kTargetBC));
-      const float sx = exp2f((float)(cum + pm) + eC - (float)(2 * kTargetBC + kTargetX));
-      const float dx = D * pow2((int)ex_s[i] - kTargetX), dec = exp2f((float)all);
+      if (k + 1 < nch) {
+        load_x(g, un, s, t0 + kL, pt, raw, xbar + pipe, halo);
+        ++xloads;
+      }
       __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + o_at;
+      smax = 0.f;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float yi[16], yx[16];
@@ -878,34 +1109,36 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
         if (in) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const uint4 xr = *reinterpret_cast<const uint4*>(X + sw128_off(i, half * 4 + 2 * r + q));
+            const uint4 xr = lds128(sX + sw128_off(i, half * 4 + 2 * r + q));
             const uint32_t xw[4] = {xr.x, xr.y, xr.z, xr.w};
             const uint4 zv = zr[2 * r + q];
             const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
             uint32_t ow[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int m = 8 * q + 2 * e;
-              const float2 xf = __half22float2(*reinterpret_cast<const __half2*>(&xw[e]));
-              float2 y;
-              y.x = fmaf(si, yi[m], fmaf(sx, yx[m], dx * xf.x));
-              y.y = fmaf(si, yi[m + 1], fmaf(sx, yx[m + 1], dx * xf.y));
-              if (a.z) {
-                const float2 zf = unpack_bf16x2(zw[e]);
-                y.x *= silu_div(zf.x);
-                y.y *= silu_div(zf.y);
-              }
+              const int c = 8 * q + 2 * e;
+              float2 y = mul2(unpack_f16x2(xw[e]), dx);
+              y = __ffma2_rn(make_float2(sx, sx), make_float2(yx[c], yx[c + 1]), y);
+              y = __ffma2_rn(make_float2(si, si), make_float2(yi[c], yi[c + 1]), y);
+              if (a.z) y = __fmul2_rn(y, silu2(unpack_bf16x2(zw[e])));
               ow[e] = pack_bf16x2(y.x, y.y);
             }
             *reinterpret_cast<uint4*>(op + 16 * r + 8 * q) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
           }
         }
         // ---- S^T <- 2^cum_L S^T + what the chunk adds
-        float ds[16];
-        tmem_ld16(tmem_at(tS, quad * 32, p0 + 16 * r), ds);
+        float add[16];
+        tmem_ld16(tmem_at(tS, quad * 32, p0 + 16 * r), add);
         tmem_ld_wait();
 #pragma unroll
-        for (int q = 0; q < 16; ++q) sv[16 * r + q] = fmaf(dec, sv[16 * r + q], ds[q]);
+        for (int q = 0; q < 16; q += 2) {
+          const float2 n2 = __ffma2_rn(make_float2(dec, dec),
+                                       make_float2(sv[16 * r + q], sv[16 * r + q + 1]),
+                                       mul2(make_float2(add[q], add[q + 1]), ds));
+          sv[16 * r + q] = n2.x;
+          sv[16 * r + q + 1] = n2.y;
+          smax = fmaxf(smax, fmaxf(fabsf(n2.x), fabsf(n2.y)));
+        }
       }
       tc_fence_before();
     }
@@ -919,6 +1152,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
     if (!ok && pt == 0) {
       report_status(a.status, GDN_ERR_TIMEOUT);
       if (mmas > 0) mbar_wait(done + pipe, (mmas - 1) & 1, g.wait_ns);
+      if (xloads > 0) mbar_wait(xbar + pipe, (xloads - 1) & 1, g.wait_ns);
     }
   }
   if (c1 == total)
@@ -964,13 +1198,13 @@ int ssm_segment(int N, int T, int pairs) {
 
 struct TcLayout {
   int seg, units;
-  size_t tiles, cb, ex, hist, state, decay, total;
+  size_t tiles, cb, ex, hist, gate, block, decay, seg_state, seg_decay, total;
 };
 
 TcLayout tc_layout(int N, int T, int H, int G, int P, int NS, int Cc) {
   TcLayout l{};
   const int pairs = G * (((H / G) * (P / 64) + 1) / 2);
-  const size_t blocks = ((size_t)T / gdn::kL + N) * G;
+  const size_t chunks = (size_t)T / gdn::kL + N, blocks = chunks * G;
   l.seg = ssm_segment(N, T, pairs);
   l.units = T / (l.seg * gdn::kL) + N;
   size_t o = 0;
@@ -978,8 +1212,11 @@ TcLayout tc_layout(int N, int T, int H, int G, int P, int NS, int Cc) {
   l.cb = o; o = up256(o + blocks * gdn::kL * gdn::kL * 2);
   l.ex = o; o = up256(o + blocks * 2 * gdn::kL);
   l.hist = o; o = up256(o + (size_t)N * 3 * Cc * 2);
-  l.state = o; o = up256(o + (size_t)l.units * H * P * NS * 4);
-  l.decay = o; o = up256(o + (size_t)l.units * H * 8);
+  l.gate = o; o = up256(o + chunks * H * 3 * gdn::kL * 4);
+  l.block = o; o = up256(o + chunks * H * 4 * 4);
+  l.decay = o; o = up256(o + chunks * H * 8);
+  l.seg_state = o; o = up256(o + (size_t)l.units * H * P * NS * 4);
+  l.seg_decay = o; o = up256(o + (size_t)l.units * H * 8);
   l.total = o;
   return l;
 }
@@ -1020,13 +1257,17 @@ cudaError_t launch_ssm_tc(gdn::SsmTcArgs g, void* workspace, cudaStream_t s) {
   g.cb = reinterpret_cast<__half*>(w + l.cb);
   g.ex = reinterpret_cast<int8_t*>(w + l.ex);
   g.hist = a.conv0 ? reinterpret_cast<__nv_bfloat16*>(w + l.hist) : nullptr;
-  g.seg_state = reinterpret_cast<float*>(w + l.state);
-  g.seg_decay = reinterpret_cast<double*>(w + l.decay);
+  g.gate = reinterpret_cast<float*>(w + l.gate);
+  g.block = reinterpret_cast<float*>(w + l.block);
+  g.decay = reinterpret_cast<double*>(w + l.decay);
+  g.seg_state = reinterpret_cast<float*>(w + l.seg_state);
+  g.seg_decay = reinterpret_cast<double*>(w + l.seg_decay);
   g.seg = l.seg;
   g.wait_ns = debug_opts().wait_limit_us ? (uint64_t)debug_opts().wait_limit_us * 1000ull
                                          : gdn::kWaitLimitNs;
   const unsigned pairs = a.G * (((a.H / a.G) * (a.P / 64) + 1) / 2);
-  cudaError_t e = launch_tc(false, gdn::ssm_bc_kernel, (unsigned)(a.T / gdn::kL + a.N) * a.G, 256,
+  const unsigned roles = a.G + (a.H + gdn::kGateHeads - 1) / gdn::kGateHeads;
+  cudaError_t e = launch_tc(false, gdn::ssm_bc_kernel, (unsigned)(a.T / gdn::kL + a.N) * roles, 256,
                             gdn::kBcSmem, s, g, "ssm_bc");
   if (e == cudaSuccess && a.T > l.seg * gdn::kL)  // a sequence may have several segments
     e = launch_tc(true, gdn::ssm_seg_kernel, (unsigned)l.units * pairs, 512, gdn::kSegSmem, s, g,
