@@ -41,66 +41,90 @@ constexpr int kL = 128;                    // chunk length
 constexpr uint32_t kTileB = 16384;         // one [128][64] 16-bit row tile
 constexpr uint32_t kBcBytes = 6 * kTileB;  // C^ | B high | B low of a (chunk, group)
 constexpr int kPipe = 256;                 // threads of one 64-channel pipeline
+constexpr int kTok = 16;                   // tokens per warp (8 warps a pipeline)
 
 // idesc of idesc_bf16 with fp16 operands (format fields 0)
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major) {
   return idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
-// tcgen05.mma issued by the lane with `lead` of a whole warp that runs this code together (the
-// descriptors stay in uniform registers: 40 products issue in 0.3 us instead of 2.3 us from a
-// single diverged thread).  mma_ss: both operands in shared memory; mma_ts: A in TMEM (row i in
-// lane i, two fp16 per 32-bit column).
-__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t adesc,
-                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// tcgen05.mma issued by the lane with `lead` of a whole warp that runs this code together.
+// Operands by the low words of their descriptors (address and LBO); the high words (SBO, version,
+// swizzle) are the same for all.  ss: both operands in shared memory; ts: A in TMEM (row i in lane
+// i, two fp16 per 32-bit column).
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
+}
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (kLayoutSW128 << 29);
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint32_t a_low,
+                                       uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
       "setp.ne.b32 e, %5, 0;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      "mov.b64 da, {%1, %6};\n\t"
+      "mov.b64 db, {%2, %6};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(lead), "n"(kDescHigh)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem,
-                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+                                       uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
       "setp.ne.b32 e, %5, 0;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      "mov.b64 db, {%2, %6};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(lead), "n"(kDescHigh)
       : "memory");
+}
+// Bounded wait for phase `parity` of `bar`; a try sleeps in hardware up to 20 us before it returns
+// (polling threads would take issue slots from the others).
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
+        : "memory");
+    if (done) return true;
+    const uint64_t t = global_timer_ns();
+    if (t0 == 0) t0 = t;
+    else if (t - t0 > limit_ns) return false;
+  }
+}
+// Read-only loads that stay where they are written: the compiler would move them up, or out of the
+// chunk loop, and spill (with 227 KB of shared memory the L1 cache holds no spills).
+__device__ __forceinline__ uint32_t ldg32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ldgf(const float* p) { return __uint_as_float(ldg32(p)); }
+__device__ __forceinline__ int ldg8(const int8_t* p) {
+  int v;
+  asm volatile("ld.global.nc.s8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ldg128(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 ldgf4(const void* p) {
+  const uint4 v = ldg128(p);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                     __uint_as_float(v.w));
 }
 // Arrive at named barrier `id` of n threads without waiting.
 __device__ __forceinline__ void bar_arrive_n(int id, int n) {
   asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-// Shared memory by 32-bit address.
-__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
-               "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
 }
 
 // One instruction each; results below 2^-126 are zero.
@@ -113,6 +137,20 @@ __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float2 v) {
   const __half2 h = __floats2half2_rn(v.x, v.y);
@@ -470,85 +508,113 @@ __device__ __forceinline__ void prefetch_row(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// The rows of a chunk's 64 channels come to shared memory as 128 bulk copies of 128 bytes, one per
-// thread of the pipeline's first four warps (the barrier counts 128 arrivals); the three rows
-// before the chunk, which only the first warp needs, to its registers.
+// The rows of a chunk's 64 channels on their way to shared memory: every warp fetches its own 16
+// tokens (so that no barrier orders them, only its own wait), and the three rows before them to
+// registers.
 __device__ __forceinline__ void load_x(const SsmTcArgs& g, const Unit& un, const Slice& s, int t0,
-                                       int pt, uint8_t* dst, uint64_t* bar, uint32_t (&halo)[3]) {
+                                       int warp, int lane, uint8_t* dst, uint32_t (&halo)[3]) {
   const SsmArgs& a = g.a;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + s.c;
-  if (pt < 128) {
-    const bool in = t0 + pt < un.e;
-    mbar_arrive_expect_tx(bar, in ? 128 : 0);
-    if (in) bulk_load(dst + pt * 128, x + (size_t)(t0 + pt) * a.Cc, 128, bar);
-  }
-  if (pt < 32) {
+  const int tw = t0 + warp * kTok;
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      const int t = t0 - 3 + q;
-      halo[q] = 0;
-      if (t >= un.s)
-        halo[q] = __ldg(reinterpret_cast<const uint32_t*>(x + (size_t)t * a.Cc) + pt);
-      else if (g.hist)
-        halo[q] = *(reinterpret_cast<const uint32_t*>(
-                        g.hist + ((size_t)un.n * 3 + 3 + t - un.s) * a.Cc + s.c) + pt);
-    }
+  for (int q = 0; q < kTok / 4; ++q) {
+    const int r = 4 * q + (lane >> 3);
+    const bool in = tw + r < un.e;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     smem_u32(dst) + (warp * kTok + r) * 128 + (lane & 7) * 16),
+                 "l"(x + (size_t)(in ? tw + r : un.s) * a.Cc + (lane & 7) * 8), "r"(in ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const int t = tw - 3 + q;
+    halo[q] = 0;
+    if (t >= un.s && t < un.e)
+      halo[q] = ldg32(reinterpret_cast<const uint32_t*>(x + (size_t)t * a.Cc) + lane);
+    else if (t < un.s && g.hist)
+      halo[q] = *(reinterpret_cast<const uint32_t*>(
+                      g.hist + ((size_t)un.n * 3 + 3 + t - un.s) * a.Cc + s.c) + lane);
   }
 }
+__device__ __forceinline__ void wait_x() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+}
 
-// Conv + SiLU of 64 channels of the warp's 16 tokens (16 w ..), lane l with channels c + 2 l and
-// c + 2 l + 1: u (zero behind the chunk's end) and the exponents of the token rows into ex_s.
-// `raw`: address of the chunk's rows.
-__device__ __forceinline__ void conv_x(const SsmTcArgs& g, const Slice& s, int L, int warp, int lane,
-                                       uint32_t raw, const uint32_t (&halo)[3], float2 (&u)[16],
-                                       int8_t* ex_s) {
-  const SsmArgs& a = g.a;
-  const int c = s.c + 2 * lane, i0 = warp * 16;
-  const uint4 wr = __ldg(reinterpret_cast<const uint4*>(
-      static_cast<const __nv_bfloat16*>(a.conv_w) + (size_t)c * 4));
+// Conv + SiLU of 64 channels of the warp's 16 tokens, lane l with channels c + 2 l and c + 2 l + 1:
+// u (zero behind the chunk's end, L) and the exponents of the token rows, into ex_s; lane q
+// returns that of its token.  `raw`: the chunk's rows.
+// The taps and the bias of a lane's two channels stay packed (5 registers, not 10).
+struct Taps {
+  uint4 w;
+  uint32_t b;
+};
+__device__ __forceinline__ Taps load_taps2(const SsmArgs& a, const Slice& s, int lane) {
+  const int c = s.c + 2 * lane;
+  Taps t{make_uint4(0, 0, 0, 0), 0};
+  t.w = ldg128(static_cast<const __nv_bfloat16*>(a.conv_w) + (size_t)c * 4);
+  if (a.conv_b) t.b = ldg32(static_cast<const __nv_bfloat16*>(a.conv_b) + c);
+  return t;
+}
+__device__ __forceinline__ int conv_x(const Taps& tp, int L, int warp, int lane, const uint8_t* raw,
+                                      const uint32_t (&halo)[3], float2 (&u)[kTok], int8_t* ex_s) {
+  uint4 wr = tp.w;
+  uint32_t br = tp.b;
+  asm volatile("" : "+r"(wr.x), "+r"(wr.y), "+r"(wr.z), "+r"(wr.w), "+r"(br));
   const float2 wa = unpack_bf16x2(wr.x), wb = unpack_bf16x2(wr.y);
   const float2 wc = unpack_bf16x2(wr.z), wd = unpack_bf16x2(wr.w);
   const float2 w0 = make_float2(wa.x, wc.x), w1 = make_float2(wa.y, wc.y);
   const float2 w2 = make_float2(wb.x, wd.x), w3 = make_float2(wb.y, wd.y);
-  float2 b = make_float2(0.f, 0.f);
-  if (a.conv_b)
-    b = unpack_bf16x2(__ldg(reinterpret_cast<const uint32_t*>(
-        static_cast<const __nv_bfloat16*>(a.conv_b) + c)));
-  const uint32_t at = raw + i0 * 128 + lane * 4;
-  const int live = L - i0;  // tokens of this warp
-  float2 h0, h1, h2;
-  if (warp == 0) {
-    h0 = unpack_bf16x2(halo[0]), h1 = unpack_bf16x2(halo[1]), h2 = unpack_bf16x2(halo[2]);
-  } else {
-    h0 = unpack_bf16x2(lds32(at - 384)), h1 = unpack_bf16x2(lds32(at - 256));
-    h2 = unpack_bf16x2(lds32(at - 128));
-  }
+  const float2 b = unpack_bf16x2(br);
+  const uint32_t* at = reinterpret_cast<const uint32_t*>(raw + warp * kTok * 128) + lane;
+  const int live = L - warp * kTok;  // tokens of this warp
+  float2 h0 = unpack_bf16x2(halo[0]), h1 = unpack_bf16x2(halo[1]), h2 = unpack_bf16x2(halo[2]);
+  uint32_t top = 0;
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const float2 v = unpack_bf16x2(lds32(at + q * 128));
+  for (int q = 0; q < kTok; ++q) {
+    const float2 v = unpack_bf16x2(at[q * 32]);
     u[q] = silu2(__ffma2_rn(w3, v, __ffma2_rn(w2, h2, __ffma2_rn(w1, h1, __ffma2_rn(w0, h0, b)))));
     h0 = h1;
     h1 = h2;
     h2 = v;
     if (q >= live) u[q] = make_float2(0.f, 0.f);
-    const float m = fmaxf(fabsf(u[q].x), fabsf(u[q].y));
-    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    if (lane == q) ex_s[i0 + q] = (int8_t)exponent_of(top);
+    const uint32_t m = __reduce_max_sync(
+        0xffffffffu, __float_as_uint(fmaxf(fabsf(u[q].x), fabsf(u[q].y))));
+    if (lane == q) top = m;
   }
+  const int e = exponent_of(top);
+  if (lane < kTok) ex_s[warp * kTok + lane] = (int8_t)e;
+  return e;
 }
 
 // B^T wX, what a chunk adds to S^T: three products of the two parts of each (the fourth is below
 // 2^-22 of the first).
+// The loops stay rolled: unrolled, all descriptors are computed before the chunk loop and spill.
 __device__ __forceinline__ void mma_state(uint32_t lead, uint32_t tS, uint32_t sB, uint32_t sW) {
-  constexpr uint32_t id = idesc_f16(128, 64, true, true);
-#pragma unroll
+#pragma unroll 1
   for (int p = 0; p < 3; ++p) {
-    const uint32_t A = sB + (p == 1 ? 2 * kTileB : 0), W = sW + (p == 2 ? kTileB : 0);
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-      mma_ss(lead, tS, desc_mnmajor(A, kk, kTileB), desc_mnmajor(W, kk, kTileB), id,
-             p > 0 || kk > 0);
+    uint32_t A = desc_low(sB + (p == 1 ? 2 * kTileB : 0), kTileB);
+    uint32_t W = desc_low(sW + (p == 2 ? kTileB : 0), kTileB);
+#pragma unroll 1
+    for (int kk = 0; kk < 8; ++kk, A += 2048 >> 4, W += 2048 >> 4)
+      mma_ss(lead, tS, A, W, idesc_f16(128, 64, true, true), (p | kk) != 0);
   }
+}
+// C S^T: C^ by rows (two row tiles of 64 columns), S^ by columns.
+__device__ __forceinline__ void mma_in(uint32_t lead, uint32_t tI, uint32_t sC, uint32_t sS) {
+  uint32_t B = desc_low(sS, kTileB);
+#pragma unroll 1
+  for (int kk = 0; kk < 8; ++kk, B += 2048 >> 4)
+    mma_ss(lead, tI, desc_low(sC + (kk >> 2) * kTileB + (kk & 3) * 32, 16), B,
+           idesc_f16(128, 64, false, true), kk != 0);
+}
+// P X: P^ in TMEM.
+__device__ __forceinline__ void mma_px(uint32_t lead, uint32_t tX, uint32_t tP, uint32_t sX) {
+  uint32_t B = desc_low(sX, kTileB);
+#pragma unroll 1
+  for (int kk = 0; kk < 8; ++kk, B += 2048 >> 4)
+    mma_ts(lead, tX, tP + kk * 8, B, idesc_f16(128, 64, false, true), kk != 0);
 }
 
 // Exponent of the largest value row i of wX may hold (w, and the rows of X and B).
@@ -556,43 +622,29 @@ __device__ __forceinline__ int weight_exponent(float w, int eX, int eB) {
   return (int)(abs_bits(w) >> 23) - 127 + eX + eB;
 }
 
-// The chunk's weights, by a whole warp: lane l has tokens 4 l .. 4 l + 3.  Puts the factors of wX
-// of the warp's own tokens 16 w .. into w_s (for this warp alone: a __syncwarp orders them) and
-// returns the chunk's exponent of wX.  Every warp of the pipeline finds the same one.
-__device__ __forceinline__ int weights(const float4& w4, uint32_t ex4, uint32_t eB4, int warp,
-                                       int lane, float* w_s) {
+// The chunk's exponent of wX, by a whole warp (lane l: tokens 4 l .. 4 l + 3; every warp of the
+// pipeline finds the same one).
+__device__ __forceinline__ int chunk_exponent(const float4& w4, uint32_t ex4, uint32_t eB4) {
   const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-  int top = INT32_MIN, eB[4];
+  int top = INT32_MIN;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    eB[e] = (int)(int8_t)(eB4 >> (8 * e));
-    top = max(top, weight_exponent(w[e], (int)(int8_t)(ex4 >> (8 * e)), eB[e]));
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((lane >> 2) == warp)
-    *reinterpret_cast<float4*>(w_s + 4 * lane) =
-        make_float4(scale2(w[0], eB[0] + kTargetW - top), scale2(w[1], eB[1] + kTargetW - top),
-                    scale2(w[2], eB[2] + kTargetW - top), scale2(w[3], eB[3] + kTargetW - top));
-  __syncwarp();
-  return top;
+  for (int e = 0; e < 4; ++e)
+    top = max(top, weight_exponent(w[e], (int)(int8_t)(ex4 >> (8 * e)), (int)(int8_t)(eB4 >> (8 * e))));
+  return __reduce_max_sync(0xffffffffu, top);
 }
 
-// Two parts of u w of the warp's 16 tokens into the row tiles at W (high) and W + kTileB (low).
-__device__ __forceinline__ void store_wx(const float2 (&u)[16], const float* w_s, int warp, int lane,
-                                         uint32_t W) {
-  const uint32_t base = W + warp * 2048 + (lane & 3) * 4, c = (lane >> 2) << 4;
+// Two parts of u w of the warp's tokens into the row tiles at W (high) and W + kTileB (low); lane q
+// has the factor of token q.
+__device__ __forceinline__ void store_wx(const float2 (&u)[kTok], float w, int warp, int lane,
+                                         uint8_t* W) {
+  const uint32_t base = warp * kTok * 128 + ((lane >> 2) << 4) + (lane & 3) * 4;
 #pragma unroll
-  for (int q = 0; q < 16; q += 4) {
-    const float4 w = *reinterpret_cast<const float4*>(w_s + warp * 16 + q);
-    const float ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t hi, lo;
-      split2(mul2(u[q + e], ws[e]), hi, lo);
-      const uint32_t at = base + (c ^ (((q + e) & 7) << 4)) + (q + e) * 128;
-      sts32(at, hi);
-      sts32(at + kTileB, lo);
-    }
+  for (int q = 0; q < kTok; ++q) {
+    uint32_t hi, lo;
+    split2(mul2(u[q], __shfl_sync(0xffffffffu, w, q)), hi, lo);
+    uint8_t* at = W + (base ^ ((q & 7) << 4)) + q * 128;
+    *reinterpret_cast<uint32_t*>(at) = hi;
+    *reinterpret_cast<uint32_t*>(at + kTileB) = lo;
   }
 }
 
@@ -623,21 +675,17 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
   uint8_t* ctl = sm + kSegCtl;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctl);      // [2] B stages landed
   uint64_t* done = full + 2;                              // [2] a pipeline's products
-  uint64_t* xbar = full + 4;                              // [2] a pipeline's x rows
   int* count = reinterpret_cast<int*>(ctl + 48);          // [2] uses of a stage, both pipelines
   int* loads = count + 2;                                 // [2] copies into it
   uint32_t* tslot = reinterpret_cast<uint32_t*>(ctl + 64);
-  float* w_s = reinterpret_cast<float*>(ctl + 128) + pipe * kL;
   // exponents of the rows of X, of two chunks: a warp may begin the next one's conv while another
   // has yet to read this one's
-  int8_t* ex2_s = reinterpret_cast<int8_t*>(ctl + 128 + 8 * kL) + pipe * 2 * kL;
+  int8_t* ex2_s = reinterpret_cast<int8_t*>(ctl + 128) + pipe * 2 * kL;
   if (tid == 0) {
     for (int k = 0; k < 4; ++k) {
       mbar_init(full + k, 1);
       count[k] = 0;  // and loads
     }
-    mbar_init(xbar, 128);
-    mbar_init(xbar + 1, 128);
     fence_barrier_init();
   }
   if (tid < 32) tmem_alloc(tslot, 128);
@@ -664,7 +712,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
   double R = 0.0;  // log2 decay of the chunks behind the current one
   float scale = 0.f;  // of the products in flight
   bool ok = true;
-  int mmas = 0, xloads = 0;
+  int mmas = 0;
   uint8_t* W = sm + kSegW + pipe * 3 * kTileB;
   uint8_t* raw = W + 2 * kTileB;
   const uint32_t sB = smem_u32(sm), sW = smem_u32(W);
@@ -672,7 +720,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
   // adds the products of chunk k (they have read wX and the stage then); the last pipeline
   // through with a stage fetches the next chunk but one into it
   auto take = [&](int k) {
-    ok = mbar_wait(done + pipe, k & 1, g.wait_ns) && ok;
+    ok = wait_long(done + pipe, k & 1, g.wait_ns) && ok;
     tc_fence_after();
     if (pt == 0 && ok) {
       __threadfence_block();
@@ -694,37 +742,39 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
   };
   if (s.live) {
     uint32_t halo[3];
-    load_x(g, un, s, un.s + (c1 - 1) * kL, pt, raw, xbar + pipe, halo);
-    xloads = 1;
+    const Taps taps = load_taps2(a, s, lane);
+    load_x(g, un, s, un.s + (c1 - 1) * kL, warp, lane, raw, halo);
     for (int k = 0; k < nch; ++k) {
-      const int ch = c1 - 1 - k, t0 = un.s + ch * kL;
+      const int ch = c1 - 1 - k, t0 = un.s + ch * kL, own = warp * kTok + (lane & (kTok - 1));
       const size_t at = (size_t)(un.chunk + ch) * a.H + s.h;
-      const float4 w4 = __ldg(reinterpret_cast<const float4*>(g.gate + at * 3 * kL) + lane);
-      const uint32_t eB4 = __ldg(reinterpret_cast<const uint32_t*>(
-          g.ex + ((size_t)(un.chunk + ch) * a.G + grp) * 2 * kL) + lane);
+      const float* gate = g.gate + at * 3 * kL;
+      const int8_t* ex = g.ex + ((size_t)(un.chunk + ch) * a.G + grp) * 2 * kL;
+      const float4 w4 = ldgf4(gate + 4 * lane);
+      const uint32_t eB4 = ldg32(ex + 4 * lane);
+      const float w = ldgf(gate + own);  // of this lane's token
+      const int eB = ldg8(ex + own);
       const double all = __ldg(g.decay + at);
       if (k + 2 < nch && pt < 128)
         prefetch_row(static_cast<const __nv_bfloat16*>(a.x) + (size_t)(t0 - 2 * kL + pt) * a.Cc + s.c);
-      ok = mbar_wait(xbar + pipe, k & 1, g.wait_ns) && ok;
-      float2 u[16];
+      wait_x();
+      float2 u[kTok];
       int8_t* ex_s = ex2_s + (k & 1) * kL;
-      conv_x(g, s, kL, warp, lane, smem_u32(raw), halo, u, ex_s);
+      conv_x(taps, kL, warp, lane, raw, halo, u, ex_s);
+      __syncwarp();  // the warp has read its rows
+      if (k + 1 < nch) load_x(g, un, s, t0 - kL, warp, lane, raw, halo);
       if (bar_or_n(1 + pipe, kPipe, !ok)) break;
-      if (k + 1 < nch) {  // every warp has read its rows
-        load_x(g, un, s, t0 - kL, pt, raw, xbar + pipe, halo);
-        ++xloads;
-      }
-      const int top = weights(w4, reinterpret_cast<const uint32_t*>(ex_s)[lane], eB4, warp, lane, w_s);
+      const int top = chunk_exponent(w4, reinterpret_cast<const uint32_t*>(ex_s)[lane], eB4);
+      const float wq = scale2(w, eB + kTargetW - top);
       if (k > 0) take(k - 1);
       scale = scale2(exp2f((float)R), top - kTargetW - kTargetB);
       R += all;
-      store_wx(u, w_s, warp, lane, sW);
+      store_wx(u, wq, warp, lane, W);
       fence_proxy_async_smem();
       if (warp != 0) {
         bar_arrive_n(3 + pipe, kPipe);
       } else {
         bar_sync_n(3 + pipe, kPipe);
-        const bool got = mbar_wait(full + (k & 1), (k >> 1) & 1, g.wait_ns);
+        const bool got = wait_long(full + (k & 1), (k >> 1) & 1, g.wait_ns);
         tc_fence_after();
         if (__all_sync(0xffffffffu, got)) {
           const uint32_t lead = elect_one();
@@ -769,15 +819,15 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
     }
     if (!ok && pt == 0) {
       report_status(a.status, GDN_ERR_TIMEOUT);
-      if (mmas > 0) mbar_wait(done + pipe, (mmas - 1) & 1, g.wait_ns);
-      mbar_wait(xbar + pipe, (xloads - 1) & 1, g.wait_ns);
+      if (mmas > 0) wait_long(done + pipe, (mmas - 1) & 1, g.wait_ns);
     }
+    wait_x();
   }
   tc_fence_before();
   __syncthreads();
   if (tid == 0)  // copies in flight, after a wait that ran out
     for (int k = 0; k < 2; ++k)
-      if (loads[k] > 0) mbar_wait(full + k, (loads[k] - 1) & 1, g.wait_ns);
+      if (loads[k] > 0) wait_long(full + k, (loads[k] - 1) & 1, g.wait_ns);
   if (tid < 32) tmem_dealloc(*tslot, 128);
 }
 
@@ -809,19 +859,17 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
   uint64_t* c_full = reinterpret_cast<uint64_t*>(ctl);
   uint64_t* b_full = c_full + 1;
   uint64_t* done = c_full + 2;  // [2] a pipeline's products of a chunk
-  uint64_t* xbar = c_full + 4;  // [2] a pipeline's x rows
   int* count = reinterpret_cast<int*>(ctl + 48);  // chunks finished, over both pipelines
   int* loads = count + 1;                         // chunks whose tiles were fetched
   uint32_t* tslot = reinterpret_cast<uint32_t*>(ctl + 56);
   uint8_t* mine = ctl + 64 + pipe * 1408;
   uint32_t* top_s = reinterpret_cast<uint32_t*>(mine);      // [8] largest magnitudes of S
-  float* w_s = reinterpret_cast<float*>(mine + 64);         // [128] factors of wX
-  float* f_s = w_s + kL;                                    // [128] F: 2^(g - maximum so far)
+  float* m_s = reinterpret_cast<float*>(mine + 64);         // [4] maxima of g of the blocks
+  float* pm_s = reinterpret_cast<float*>(mine + 128);       // [128] running maximum of g
+  __half* f_s = reinterpret_cast<__half*>(pm_s + kL);       // [128] F: 2^(g - maximum of the block)
   int8_t* ex_s = reinterpret_cast<int8_t*>(f_s + kL);       // [128] exponents of the rows of X
   if (tid == 0) {
     for (int k = 0; k < 4; ++k) mbar_init(c_full + k, 1);
-    mbar_init(xbar, 128);
-    mbar_init(xbar + 1, 128);
     *count = *loads = 0;
     fence_barrier_init();
   }
@@ -879,38 +927,30 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
   }
   {
     // P above the diagonal blocks is zero throughout
-    float zero[32];
-#pragma unroll
-    for (int q = 0; q < 32; ++q) zero[q] = 0.f;
-    tmem_st32(tmem_at(tP, quad * 32, half * 32), zero);
+    const uint32_t zero[16] = {};
+    tmem_st16(tmem_at(tP, quad * 32, p0), zero);
+    tmem_st16(tmem_at(tP, quad * 32, p0 + 16), zero);
     tmem_st_wait();
   }
   uint8_t* X = sm + kMainPipe + pipe * 4 * kTileB;
-  uint8_t* raw = X + 3 * kTileB;
-  const uint32_t sC = smem_u32(sm), sX = smem_u32(X), sW = sX + kTileB, sS = sX + 3 * kTileB;
+  uint8_t* W = X + kTileB;
+  uint8_t* S16 = X + 3 * kTileB;  // and the next chunk's rows of x
+  const uint32_t sC = smem_u32(sm), sX = smem_u32(X), sW = smem_u32(W), sS = smem_u32(S16);
   const int warp = __shfl_sync(0xffffffffu, pw, 0);  // the same for the whole warp
   bool ok = true;
-  int mmas = 0, xloads = 0;
+  int mmas = 0;
   float smax = 0.f;  // largest magnitude of this thread's part of S
 #pragma unroll
   for (int q = 0; q < 32; ++q) smax = fmaxf(smax, fabsf(sv[q]));
   if (s.live) {
     uint32_t halo[3];
-    if (nch > 0) {
-      load_x(g, un, s, un.s + c0 * kL, pt, raw, xbar + pipe, halo);
-      xloads = 1;
-    }
+    const Taps taps = load_taps2(a, s, lane);
+    if (nch > 0) load_x(g, un, s, un.s + c0 * kL, warp, lane, S16, halo);
     for (int k = 0; k < nch; ++k) {
       const int t0 = un.s + (c0 + k) * kL, L = min(kL, un.e - t0);
       const size_t chunk = (size_t)(un.chunk + c0 + k), at = chunk * a.G + grp;
       const float* gate = g.gate + (chunk * a.H + s.h) * 3 * kL;
       const int8_t* ex = g.ex + at * 2 * kL;
-      const float4 w4 = __ldg(reinterpret_cast<const float4*>(gate) + lane);
-      const float4 lf4 = __ldg(reinterpret_cast<const float4*>(gate + kL) + lane);
-      const float lf = __ldg(gate + kL + i), cum = __ldg(gate + 2 * kL + i);
-      const float4 bt = __ldg(reinterpret_cast<const float4*>(g.block) + chunk * a.H + s.h);
-      const uint32_t eB4 = __ldg(reinterpret_cast<const uint32_t*>(ex) + lane);
-      const int eB = __ldg(ex + i), eC = __ldg(ex + kL + i);
       if (t0 + kL + i < un.e && k + 1 < nch) {  // the next chunk's inputs on their way
         const size_t t1 = (size_t)t0 + kL + i;
         if (half == 0) prefetch_row(static_cast<const __nv_bfloat16*>(a.x) + t1 * a.Cc + s.c);
@@ -918,18 +958,17 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
           prefetch_row(static_cast<const __nv_bfloat16*>(a.z) + t1 * a.H * a.P + s.c);
       }
       // ---- conv of X; the largest magnitude of S
-      ok = mbar_wait(xbar + pipe, k & 1, g.wait_ns) && ok;
-      float2 u[16];
-      conv_x(g, s, L, warp, lane, sS, halo, u, ex_s);
+      wait_x();
+      float2 u[kTok];
+      const int eq = conv_x(taps, L, warp, lane, S16, halo, u, ex_s);
       uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));
+      const float4 w4 = ldgf4(gate + 4 * lane);
+      const uint32_t eB4 = ldg32(ex + 4 * lane);
+      const float w = ldgf(gate + warp * kTok + (lane & (kTok - 1)));
       if (lane == 0) top_s[warp] = top;
       if (bar_or_n(1 + pipe, kPipe, !ok)) break;
       // ---- S^ = fp16 operand of C S^T
-      {
-        const uint4 ta = *reinterpret_cast<const uint4*>(top_s);
-        const uint4 tb = *reinterpret_cast<const uint4*>(top_s + 4);
-        top = max(max(max(ta.x, ta.y), max(ta.z, ta.w)), max(max(tb.x, tb.y), max(tb.z, tb.w)));
-      }
+      top = __reduce_max_sync(0xffffffffu, top_s[lane & 7]);
       const int eS = exponent_of(top);
       {
         const float sc = pow2(kTargetS - eS);
@@ -940,101 +979,119 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
           f.y = pack_f16x2(mul2(make_float2(sv[8 * q + 2], sv[8 * q + 3]), sc));
           f.z = pack_f16x2(mul2(make_float2(sv[8 * q + 4], sv[8 * q + 5]), sc));
           f.w = pack_f16x2(mul2(make_float2(sv[8 * q + 6], sv[8 * q + 7]), sc));
-          sts128(sS + sw128_off(i, half * 4 + q), f);
+          *reinterpret_cast<uint4*>(S16 + sw128_off(i, half * 4 + q)) = f;
         }
       }
       // ---- weights of wX; X^ and wX
       const uint32_t ex4 = reinterpret_cast<const uint32_t*>(ex_s)[lane];
-      const int wt = weights(w4, ex4, eB4, warp, lane, w_s);
-      store_wx(u, w_s, warp, lane, sW);
+      const int wt = chunk_exponent(w4, ex4, eB4);
       {
-        const uint32_t base = sX + warp * 2048 + (lane & 3) * 4, c = (lane >> 2) << 4;
+        const int own = warp * kTok + (lane & (kTok - 1));
+        const uint32_t e4 = __shfl_sync(0xffffffffu, eB4, own >> 2);
+        const int eB = (int)(int8_t)(e4 >> (8 * (own & 3)));
+        store_wx(u, scale2(w, eB + kTargetW - wt), warp, lane, W);
+        const float xs = pow2(kTargetX - eq);
+        const uint32_t base = warp * kTok * 128 + ((lane >> 2) << 4) + (lane & 3) * 4;
 #pragma unroll
-        for (int q = 0; q < 16; q += 4) {
-          const uint32_t e4 = *reinterpret_cast<const uint32_t*>(ex_s + warp * 16 + q);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            sts32(base + (c ^ (((q + e) & 7) << 4)) + (q + e) * 128,
-                  pack_f16x2(mul2(u[q + e], pow2(kTargetX - (int)(int8_t)(e4 >> (8 * e))))));
-        }
+        for (int q = 0; q < kTok; ++q)
+          *reinterpret_cast<uint32_t*>(X + (base ^ ((q & 7) << 4)) + q * 128) =
+              pack_f16x2(mul2(u[q], __shfl_sync(0xffffffffu, xs, q)));
       }
-      // ---- g of token i and its running maximum, in units of its block's start; the maxima M of
-      // the blocks (lane l: tokens 4 l ..), and what they are from this block on (ref)
+      // ---- g of token i, in units of its block's start
+      const float4 bt = ldgf4(g.block + (chunk * a.H + s.h) * 4);
       const int eX = ex_s[i];
-      const float gi = lf + (float)(eX + eB);
-      float pm = gi;
+      const float gi = ldgf(gate + kL + i) + (float)(eX + ldg8(ex + i));
+      if (half == 0) {
+        // its running maximum, and the maxima M of the blocks (lane l: tokens 4 l ..)
+        const float4 lf4 = ldgf4(gate + kL + 4 * lane);
+        float pm = gi;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float up = __shfl_up_sync(0xffffffffu, pm, o);
-        if (lane >= o) pm = fmaxf(pm, up);
-      }
-      float gm;
-      {
+        for (int o = 1; o < 32; o <<= 1) {
+          const float up = __shfl_up_sync(0xffffffffu, pm, o);
+          if (lane >= o) pm = fmaxf(pm, up);
+        }
         const float l4[4] = {lf4.x, lf4.y, lf4.z, lf4.w};
-        gm = -INFINITY;
+        float gm = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           gm = fmaxf(gm, l4[e] + (float)((int)(int8_t)(ex4 >> (8 * e)) + (int)(int8_t)(eB4 >> (8 * e))));
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+        const float M0 = __shfl_sync(0xffffffffu, gm, 0);
+        const float M1 = fmaxf(M0 + bt.x, __shfl_sync(0xffffffffu, gm, 8));
+        const float M2 = fmaxf(M1 + bt.y, __shfl_sync(0xffffffffu, gm, 16));
+        const float M3 = fmaxf(M2 + bt.z, __shfl_sync(0xffffffffu, gm, 24));
+        if (quad == 1) pm = fmaxf(pm, M0 + bt.x);
+        if (quad == 2) pm = fmaxf(pm, M1 + bt.y);
+        if (quad == 3) pm = fmaxf(pm, M2 + bt.z);
+        pm_s[i] = pm;
+        f_s[i] = __float2half_rn(ex2(gi - (quad == 0 ? M0 : (quad == 1 ? M1 : (quad == 2 ? M2 : M3)))));
+        if (pt == 0) *reinterpret_cast<float4*>(m_s) = make_float4(M0, M1, M2, M3);
       }
-      const float M0 = __shfl_sync(0xffffffffu, gm, 0);
-      const float M1 = fmaxf(M0 + bt.x, __shfl_sync(0xffffffffu, gm, 8));
-      const float M2 = fmaxf(M1 + bt.y, __shfl_sync(0xffffffffu, gm, 16));
-      const float M3 = fmaxf(M2 + bt.z, __shfl_sync(0xffffffffu, gm, 24));
-      float ref[3], cs, Mq;  // cs: decay up to this block
-      if (quad == 0) {
-        cs = 0.f, Mq = M0, ref[0] = ref[1] = ref[2] = 0.f;
-      } else if (quad == 1) {
-        cs = bt.x, Mq = M1, ref[0] = M0 + bt.x, ref[1] = ref[2] = 0.f;
-        pm = fmaxf(pm, ref[0]);
-      } else if (quad == 2) {
-        cs = bt.x + bt.y, Mq = M2, ref[0] = M0 + (bt.x + bt.y), ref[1] = M1 + bt.y, ref[2] = 0.f;
-        pm = fmaxf(pm, ref[1]);
-      } else {
-        cs = bt.x + (bt.y + bt.z), Mq = M3, ref[0] = M0 + cs, ref[1] = M1 + (bt.y + bt.z);
-        ref[2] = M2 + bt.z;
-        pm = fmaxf(pm, ref[2]);
+      // C B^T of this thread's columns: 16 of each block of 32 up to the diagonal
+      // (two blocks ahead)
+      const __half* cb = g.cb + (at * kL + i) * kL + half * 16;
+      uint4 cbr[2][2];
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        if (blk <= quad) {
+          cbr[blk][0] = ldg128(cb + blk * 32);
+          cbr[blk][1] = ldg128(cb + blk * 32 + 8);
+        }
       }
-      if (half == 0) f_s[i] = ex2(gi - Mq);
       fence_proxy_async_smem();
       tc_fence_before();
       bar_sync_n(1 + pipe, kPipe);
       if (warp == 0) {
-        const bool got = mbar_wait(c_full, k & 1, g.wait_ns) && mbar_wait(b_full, k & 1, g.wait_ns);
+        const bool got = wait_long(c_full, k & 1, g.wait_ns) && wait_long(b_full, k & 1, g.wait_ns);
         tc_fence_after();
         if (__all_sync(0xffffffffu, got)) {
           const uint32_t lead = elect_one();
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ss(lead, tI, desc_kmajor(sC, kk, kTileB), desc_mnmajor(sS, kk, kTileB),
-                   idesc_f16(128, 64, false, true), kk > 0);
+          mma_in(lead, tI, sC, sS);
           mma_state(lead, tS, sC + 2 * kTileB, sW);
         } else {
           ok = false;
         }
         __syncwarp();
       }
-      // ---- P^ (fp16) into TMEM: this thread has 16 columns of each block of 32 up to the diagonal
+      // ---- P^ (fp16) into TMEM.  ref: the blocks' maxima from this block's start on; cs: decay up
+      // to this block
+      const float pm = pm_s[i];
+      float cs = 0.f;
       {
-        const __half* cb = g.cb + (at * kL + i) * kL + half * 16;
+        const float4 M = *reinterpret_cast<const float4*>(m_s);
+        float ref[3] = {0.f, 0.f, 0.f};
+        if (quad == 1) {
+          cs = bt.x, ref[0] = M.x + bt.x;
+        } else if (quad == 2) {
+          cs = bt.x + bt.y, ref[0] = M.x + (bt.x + bt.y), ref[1] = M.y + bt.y;
+        } else if (quad == 3) {
+          cs = bt.x + (bt.y + bt.z), ref[0] = M.x + cs, ref[1] = M.y + (bt.y + bt.z);
+          ref[2] = M.z + bt.z;
+        }
 #pragma unroll
         for (int blk = 0; blk < 4; ++blk) {
           if (blk <= quad) {
-            const uint4 r0 = __ldg(reinterpret_cast<const uint4*>(cb + blk * 32));
-            const uint4 r1 = __ldg(reinterpret_cast<const uint4*>(cb + blk * 32 + 8));
+            const uint4 r0 = cbr[blk & 1][0], r1 = cbr[blk & 1][1];
             const uint32_t in[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+            if (blk + 2 <= quad) {
+              cbr[blk & 1][0] = ldg128(cb + (blk + 2) * 32);
+              cbr[blk & 1][1] = ldg128(cb + (blk + 2) * 32 + 8);
+            }
             uint32_t out[8];
             const int j0 = blk * 32 + half * 16;
             if (blk < quad) {
-              const float rf = ex2(ref[blk < 3 ? blk : 2] - pm);
+              const __half2 rf = __float2half2_rn(ex2(ref[blk < 3 ? blk : 2] - pm));
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float4 f = *reinterpret_cast<const float4*>(f_s + j0 + 4 * q);
-                out[2 * q] = pack_f16x2(
-                    __fmul2_rn(unpack_f16x2(in[2 * q]), mul2(make_float2(f.x, f.y), rf)));
-                out[2 * q + 1] = pack_f16x2(
-                    __fmul2_rn(unpack_f16x2(in[2 * q + 1]), mul2(make_float2(f.z, f.w), rf)));
+              for (int p = 0; p < 2; ++p) {
+                const uint4 fr = *reinterpret_cast<const uint4*>(f_s + j0 + 8 * p);
+                const uint32_t f[4] = {fr.x, fr.y, fr.z, fr.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&in[4 * p + q]),
+                                            __hmul2(*reinterpret_cast<const __half2*>(&f[q]), rf));
+                  out[4 * p + q] = *reinterpret_cast<const uint32_t*>(&v);
+                }
               }
             } else {
               // the diagonal block: g of its tokens is in the lanes of this warp
@@ -1061,10 +1118,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
         tc_fence_after();
         if (__all_sync(0xffffffffu, ok)) {
           const uint32_t lead = elect_one();
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(lead, tX, tP + kk * 8, desc_mnmajor(sX, kk, kTileB),
-                   idesc_f16(128, 64, false, true), kk > 0);
+          mma_px(lead, tX, tP, sX);
           if (lead) mma_commit(done + pipe);
           ++mmas;
         }
@@ -1073,18 +1127,20 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
       // ---- outputs
       const bool in = i < L;
       const size_t o_at = ((size_t)(t0 + i) * a.H) * a.P + s.c + p0;
-      uint4 zr[4];
+      const __nv_bfloat16* zp = static_cast<const __nv_bfloat16*>(a.z) + o_at;
+      uint4 zr[2] = {};  // two quarters ahead
       if (a.z && in) {
-        const uint4* zp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.z) + o_at);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) zr[q] = __ldg(zp + q);
+        zr[0] = ldg128(zp);
+        zr[1] = ldg128(zp + 8);
       }
+      const float cum = ldgf(gate + 2 * kL + i);
+      const int eC = ldg8(ex + kL + i);
       const float dec = exp2f((float)__ldg(g.decay + chunk * a.H + s.h));
       const float si = ex2(cs + cum + (float)(eC + eS - kTargetS - kTargetC));
       const float sx = ex2((cum + pm) + (float)(eC - kTargetC - kTargetB - kScaleCB - kTargetX));
       const float dx = D * pow2(eX - kTargetX);
       const float ds = scale2(1.f, wt - kTargetW - kTargetB);
-      ok = mbar_wait(done + pipe, k & 1, g.wait_ns) && ok;
+      ok = wait_long(done + pipe, k & 1, g.wait_ns) && ok;
       tc_fence_after();
       if (pt == 0 && ok) {  // the last pipeline through with the tiles fetches the next ones
         __threadfence_block();
@@ -1094,49 +1150,43 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
         }
       }
       __syncwarp();
-      if (k + 1 < nch) {
-        load_x(g, un, s, t0 + kL, pt, raw, xbar + pipe, halo);
-        ++xloads;
-      }
+      if (k + 1 < nch) load_x(g, un, s, t0 + kL, warp, lane, S16, halo);
       __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + o_at;
       smax = 0.f;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float yi[16], yx[16];
-        tmem_ld16(tmem_at(tI, quad * 32, p0 + 16 * r), yi);
-        tmem_ld16(tmem_at(tX, quad * 32, p0 + 16 * r), yx);
+      for (int r = 0; r < 4; ++r) {
+        float yi[8], yx[8];
+        tmem_ld8(tmem_at(tI, quad * 32, p0 + 8 * r), yi);
+        tmem_ld8(tmem_at(tX, quad * 32, p0 + 8 * r), yx);
         tmem_ld_wait();
         if (in) {
+          const uint4 xr = *reinterpret_cast<const uint4*>(X + sw128_off(i, half * 4 + r));
+          const uint32_t xw[4] = {xr.x, xr.y, xr.z, xr.w};
+          const uint4 zv = zr[r & 1];
+          const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
+          if (r < 2 && a.z) zr[r] = ldg128(zp + 8 * (r + 2));
+          uint32_t ow[4];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint4 xr = lds128(sX + sw128_off(i, half * 4 + 2 * r + q));
-            const uint32_t xw[4] = {xr.x, xr.y, xr.z, xr.w};
-            const uint4 zv = zr[2 * r + q];
-            const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
-            uint32_t ow[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int c = 8 * q + 2 * e;
-              float2 y = mul2(unpack_f16x2(xw[e]), dx);
-              y = __ffma2_rn(make_float2(sx, sx), make_float2(yx[c], yx[c + 1]), y);
-              y = __ffma2_rn(make_float2(si, si), make_float2(yi[c], yi[c + 1]), y);
-              if (a.z) y = __fmul2_rn(y, silu2(unpack_bf16x2(zw[e])));
-              ow[e] = pack_bf16x2(y.x, y.y);
-            }
-            *reinterpret_cast<uint4*>(op + 16 * r + 8 * q) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+          for (int e = 0; e < 4; ++e) {
+            float2 y = mul2(unpack_f16x2(xw[e]), dx);
+            y = __ffma2_rn(make_float2(sx, sx), make_float2(yx[2 * e], yx[2 * e + 1]), y);
+            y = __ffma2_rn(make_float2(si, si), make_float2(yi[2 * e], yi[2 * e + 1]), y);
+            if (a.z) y = __fmul2_rn(y, silu2(unpack_bf16x2(zw[e])));
+            ow[e] = pack_bf16x2(y.x, y.y);
           }
+          *reinterpret_cast<uint4*>(op + 8 * r) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
         }
         // ---- S^T <- 2^cum_L S^T + what the chunk adds
-        float add[16];
-        tmem_ld16(tmem_at(tS, quad * 32, p0 + 16 * r), add);
+        float add[8];
+        tmem_ld8(tmem_at(tS, quad * 32, p0 + 8 * r), add);
         tmem_ld_wait();
 #pragma unroll
-        for (int q = 0; q < 16; q += 2) {
+        for (int q = 0; q < 8; q += 2) {
           const float2 n2 = __ffma2_rn(make_float2(dec, dec),
-                                       make_float2(sv[16 * r + q], sv[16 * r + q + 1]),
+                                       make_float2(sv[8 * r + q], sv[8 * r + q + 1]),
                                        mul2(make_float2(add[q], add[q + 1]), ds));
-          sv[16 * r + q] = n2.x;
-          sv[16 * r + q + 1] = n2.y;
+          sv[8 * r + q] = n2.x;
+          sv[8 * r + q + 1] = n2.y;
           smax = fmaxf(smax, fmaxf(fabsf(n2.x), fabsf(n2.y)));
         }
       }
@@ -1151,17 +1201,17 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
     }
     if (!ok && pt == 0) {
       report_status(a.status, GDN_ERR_TIMEOUT);
-      if (mmas > 0) mbar_wait(done + pipe, (mmas - 1) & 1, g.wait_ns);
-      if (xloads > 0) mbar_wait(xbar + pipe, (xloads - 1) & 1, g.wait_ns);
+      if (mmas > 0) wait_long(done + pipe, (mmas - 1) & 1, g.wait_ns);
     }
+    wait_x();
   }
   if (c1 == total)
     conv_history<__nv_bfloat16>(a, un.n, row, un.s, un.e, blockIdx.x % (a.G * pairs), a.G * pairs);
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *loads > 0) {  // copies in flight, after a wait that ran out
-    mbar_wait(c_full, (*loads - 1) & 1, g.wait_ns);
-    mbar_wait(b_full, (*loads - 1) & 1, g.wait_ns);
+    wait_long(c_full, (*loads - 1) & 1, g.wait_ns);
+    wait_long(b_full, (*loads - 1) & 1, g.wait_ns);
   }
   if (tid < 32) tmem_dealloc(tmem, 512);
 }
