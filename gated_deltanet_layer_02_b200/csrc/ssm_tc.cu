@@ -122,6 +122,10 @@ __device__ __forceinline__ float4 ldgf4(const void* p) {
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
                      __uint_as_float(v.w));
 }
+// The same value in every lane, in a uniform register (the reduction's result is one): the chunk
+// loops keep their indices there and all vector registers for data.
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
 // Arrive at named barrier `id` of n threads without waiting.
 __device__ __forceinline__ void bar_arrive_n(int id, int n) {
   asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
@@ -260,13 +264,9 @@ __device__ __forceinline__ Unit find_unit(const SsmArgs& a, int tokens, bool emp
     const uint32_t who = __ballot_sync(0xffffffffu, mine);
     if (who) {
       const int l = __ffs(who) - 1;
-      r.n = __shfl_sync(0xffffffffu, r.n, l);
-      r.j = __shfl_sync(0xffffffffu, r.j, l);
-      r.s = __shfl_sync(0xffffffffu, r.s, l);
-      r.e = __shfl_sync(0xffffffffu, r.e, l);
-      r.chunk = __shfl_sync(0xffffffffu, r.chunk, l);
-      r.first = __shfl_sync(0xffffffffu, r.first, l);
-      return r;
+      const bool it = lane == l;
+      return Unit{uniform(it ? r.n : -1), uniform(it ? r.j : 0),     uniform(it ? r.s : 0),
+                  uniform(it ? r.e : 0),  uniform(it ? r.chunk : 0), uniform(it ? r.first : 0)};
     }
     u0 += __shfl_sync(0xffffffffu, ui, 31);
     c0 += __shfl_sync(0xffffffffu, ci, 31);
@@ -543,8 +543,8 @@ __device__ __forceinline__ void wait_x() {
 }
 
 // Conv + SiLU of 64 channels of the warp's 16 tokens, lane l with channels c + 2 l and c + 2 l + 1:
-// u (zero behind the chunk's end, L) and the exponents of the token rows, into ex_s; lane q
-// returns that of its token.  `raw`: the chunk's rows.
+// put(q, u) takes token q's values (zero behind the chunk's end, L); the exponents of the token
+// rows go to ex_s, and lane q returns that of its token.  `raw`: the chunk's rows.
 // The taps and the bias of a lane's two channels stay packed (5 registers, not 10).
 struct Taps {
   uint4 w;
@@ -557,8 +557,9 @@ __device__ __forceinline__ Taps load_taps2(const SsmArgs& a, const Slice& s, int
   if (a.conv_b) t.b = ldg32(static_cast<const __nv_bfloat16*>(a.conv_b) + c);
   return t;
 }
+template <typename Put>
 __device__ __forceinline__ int conv_x(const Taps& tp, int L, int warp, int lane, const uint8_t* raw,
-                                      const uint32_t (&halo)[3], float2 (&u)[kTok], int8_t* ex_s) {
+                                      const uint32_t (&halo)[3], int8_t* ex_s, Put&& put) {
   uint4 wr = tp.w;
   uint32_t br = tp.b;
   asm volatile("" : "+r"(wr.x), "+r"(wr.y), "+r"(wr.z), "+r"(wr.w), "+r"(br));
@@ -574,13 +575,15 @@ __device__ __forceinline__ int conv_x(const Taps& tp, int L, int warp, int lane,
 #pragma unroll
   for (int q = 0; q < kTok; ++q) {
     const float2 v = unpack_bf16x2(at[q * 32]);
-    u[q] = silu2(__ffma2_rn(w3, v, __ffma2_rn(w2, h2, __ffma2_rn(w1, h1, __ffma2_rn(w0, h0, b)))));
+    float2 u =
+        silu2(__ffma2_rn(w3, v, __ffma2_rn(w2, h2, __ffma2_rn(w1, h1, __ffma2_rn(w0, h0, b)))));
     h0 = h1;
     h1 = h2;
     h2 = v;
-    if (q >= live) u[q] = make_float2(0.f, 0.f);
-    const uint32_t m = __reduce_max_sync(
-        0xffffffffu, __float_as_uint(fmaxf(fabsf(u[q].x), fabsf(u[q].y))));
+    if (q >= live) u = make_float2(0.f, 0.f);
+    put(q, u);
+    const uint32_t m =
+        __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(u.x), fabsf(u.y))));
     if (lane == q) top = m;
   }
   const int e = exponent_of(top);
@@ -590,31 +593,36 @@ __device__ __forceinline__ int conv_x(const Taps& tp, int L, int warp, int lane,
 
 // B^T wX, what a chunk adds to S^T: three products of the two parts of each (the fourth is below
 // 2^-22 of the first).
-// The loops stay rolled: unrolled, all descriptors are computed before the chunk loop and spill.
+// (In these three the base addresses are made opaque: as loop invariants all descriptors would be
+// computed before the chunk loop, and spill.)
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
 __device__ __forceinline__ void mma_state(uint32_t lead, uint32_t tS, uint32_t sB, uint32_t sW) {
-#pragma unroll 1
-  for (int p = 0; p < 3; ++p) {
-    uint32_t A = desc_low(sB + (p == 1 ? 2 * kTileB : 0), kTileB);
-    uint32_t W = desc_low(sW + (p == 2 ? kTileB : 0), kTileB);
-#pragma unroll 1
-    for (int kk = 0; kk < 8; ++kk, A += 2048 >> 4, W += 2048 >> 4)
-      mma_ss(lead, tS, A, W, idesc_f16(128, 64, true, true), (p | kk) != 0);
-  }
+  const uint32_t A = opaque(desc_low(sB, kTileB)), W = opaque(desc_low(sW, kTileB));
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      mma_ss(lead, tS, A + (((p == 1 ? 2 * kTileB : 0) + kk * 2048) >> 4),
+             W + (((p == 2 ? kTileB : 0) + kk * 2048) >> 4), idesc_f16(128, 64, true, true),
+             (p | kk) != 0);
 }
 // C S^T: C^ by rows (two row tiles of 64 columns), S^ by columns.
 __device__ __forceinline__ void mma_in(uint32_t lead, uint32_t tI, uint32_t sC, uint32_t sS) {
-  uint32_t B = desc_low(sS, kTileB);
-#pragma unroll 1
-  for (int kk = 0; kk < 8; ++kk, B += 2048 >> 4)
-    mma_ss(lead, tI, desc_low(sC + (kk >> 2) * kTileB + (kk & 3) * 32, 16), B,
+  const uint32_t A = opaque(desc_low(sC, 16)), B = opaque(desc_low(sS, kTileB));
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ss(lead, tI, A + (((kk >> 2) * kTileB + (kk & 3) * 32) >> 4), B + ((kk * 2048) >> 4),
            idesc_f16(128, 64, false, true), kk != 0);
 }
 // P X: P^ in TMEM.
 __device__ __forceinline__ void mma_px(uint32_t lead, uint32_t tX, uint32_t tP, uint32_t sX) {
-  uint32_t B = desc_low(sX, kTileB);
-#pragma unroll 1
-  for (int kk = 0; kk < 8; ++kk, B += 2048 >> 4)
-    mma_ts(lead, tX, tP + kk * 8, B, idesc_f16(128, 64, false, true), kk != 0);
+  const uint32_t B = opaque(desc_low(sX, kTileB));
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts(lead, tX, tP + kk * 8, B + ((kk * 2048) >> 4), idesc_f16(128, 64, false, true), kk != 0);
 }
 
 // Exponent of the largest value row i of wX may hold (w, and the rows of X and B).
@@ -633,19 +641,17 @@ __device__ __forceinline__ int chunk_exponent(const float4& w4, uint32_t ex4, ui
   return __reduce_max_sync(0xffffffffu, top);
 }
 
-// Two parts of u w of the warp's tokens into the row tiles at W (high) and W + kTileB (low); lane q
-// has the factor of token q.
-__device__ __forceinline__ void store_wx(const float2 (&u)[kTok], float w, int warp, int lane,
-                                         uint8_t* W) {
-  const uint32_t base = warp * kTok * 128 + ((lane >> 2) << 4) + (lane & 3) * 4;
-#pragma unroll
-  for (int q = 0; q < kTok; ++q) {
-    uint32_t hi, lo;
-    split2(mul2(u[q], __shfl_sync(0xffffffffu, w, q)), hi, lo);
-    uint8_t* at = W + (base ^ ((q & 7) << 4)) + q * 128;
-    *reinterpret_cast<uint32_t*>(at) = hi;
-    *reinterpret_cast<uint32_t*>(at + kTileB) = lo;
-  }
+// Byte offset of the warp's token q and the lane's channel pair in a [128][64] row tile; the 16-byte
+// pieces of row r are swizzled by r % 8.
+__device__ __forceinline__ uint32_t pair_off(int warp, int lane, int q) {
+  return ((warp * kTok * 128 + ((lane >> 2) << 4) + (lane & 3) * 4) ^ ((q & 7) << 4)) + q * 128;
+}
+// Two parts of u w into the tiles at W (high) and W + kTileB (low).
+__device__ __forceinline__ void store_parts(float2 u, float w, uint8_t* W, uint32_t at) {
+  uint32_t hi, lo;
+  split2(mul2(u, w), hi, lo);
+  *reinterpret_cast<uint32_t*>(W + at) = hi;
+  *reinterpret_cast<uint32_t*>(W + at + kTileB) = lo;
 }
 
 // ------------------------------------------------------------------------------------ seg
@@ -671,7 +677,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
   const int c0 = un.j * g.seg, c1 = c0 + g.seg;
   if (c1 >= total) return;  // no segment follows
 
-  const int pipe = tid >> 8, pt = tid & 255, pw = pt >> 5;
+  const int wid = uniform(tid >> 5), pipe = wid >> 3, pw = wid & 7, pt = tid & 255;
   uint8_t* ctl = sm + kSegCtl;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctl);      // [2] B stages landed
   uint64_t* done = full + 2;                              // [2] a pipeline's products
@@ -691,7 +697,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
   if (tid < 32) tmem_alloc(tslot, 128);
   __syncthreads();
   tc_fence_after();
-  const uint32_t tS = *tslot + pipe * 64;
+  const uint32_t tmem = (uint32_t)uniform((int)*tslot), tS = tmem + pipe * 64;
   const Slice s = slice_of(g, grp, 2 * pair + pipe, slices);
   const int users = min(2, slices - 2 * pair);
   const int nch = c1 - c0;
@@ -716,7 +722,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
   uint8_t* W = sm + kSegW + pipe * 3 * kTileB;
   uint8_t* raw = W + 2 * kTileB;
   const uint32_t sB = smem_u32(sm), sW = smem_u32(W);
-  const int warp = __shfl_sync(0xffffffffu, pw, 0);  // the same for the whole warp
+  const int warp = pw;
   // adds the products of chunk k (they have read wX and the stage then); the last pipeline
   // through with a stage fetches the next chunk but one into it
   auto take = [&](int k) {
@@ -759,7 +765,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
       wait_x();
       float2 u[kTok];
       int8_t* ex_s = ex2_s + (k & 1) * kL;
-      conv_x(taps, kL, warp, lane, raw, halo, u, ex_s);
+      conv_x(taps, kL, warp, lane, raw, halo, ex_s, [&](int q, float2 v) { u[q] = v; });
       __syncwarp();  // the warp has read its rows
       if (k + 1 < nch) load_x(g, un, s, t0 - kL, warp, lane, raw, halo);
       if (bar_or_n(1 + pipe, kPipe, !ok)) break;
@@ -768,7 +774,9 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
       if (k > 0) take(k - 1);
       scale = scale2(exp2f((float)R), top - kTargetW - kTargetB);
       R += all;
-      store_wx(u, wq, warp, lane, W);
+#pragma unroll
+      for (int q = 0; q < kTok; ++q)
+        store_parts(u[q], __shfl_sync(0xffffffffu, wq, q), W, pair_off(warp, lane, q));
       fence_proxy_async_smem();
       if (warp != 0) {
         bar_arrive_n(3 + pipe, kPipe);
@@ -828,7 +836,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
   if (tid == 0)  // copies in flight, after a wait that ran out
     for (int k = 0; k < 2; ++k)
       if (loads[k] > 0) wait_long(full + k, (loads[k] - 1) & 1, g.wait_ns);
-  if (tid < 32) tmem_dealloc(*tslot, 128);
+  if (tid < 32) tmem_dealloc(tmem, 128);
 }
 
 // ----------------------------------------------------------------------------------- main
@@ -854,7 +862,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
     pdl_wait();
     return;
   }
-  const int pipe = tid >> 8, pt = tid & 255, pw = pt >> 5;
+  const int wid = uniform(tid >> 5), pipe = wid >> 3, pw = wid & 7, pt = tid & 255;
   uint8_t* ctl = sm + kMainCtl;
   uint64_t* c_full = reinterpret_cast<uint64_t*>(ctl);
   uint64_t* b_full = c_full + 1;
@@ -876,14 +884,14 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
   if (tid < 32) tmem_alloc(tslot, 512);
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tslot);
   const uint32_t tS = tmem + pipe * 64, tI = tmem + 128 + pipe * 128, tX = tI + 64;
   const uint32_t tP = tmem + 384 + pipe * 64;
   const Slice s = slice_of(g, grp, 2 * pair + pipe, slices);
   const int users = min(2, slices - 2 * pair);
   const int total = (un.e - un.s + kL - 1) / kL;
   const int c0 = un.j * g.seg, c1 = min(total, c0 + g.seg), nch = c1 - c0;
-  const int row = state_row(a.slot, un.n, a.num_slots);
+  const int row = uniform(state_row(a.slot, un.n, a.num_slots));
   if (row < 0 && tid == 0) report_status(a.status, GDN_ERR_INVALID_ARG);
   const float D = a.D ? a.D[s.h] : 0.f;
   const int quad = pw & 3, half = pw >> 2;
@@ -936,7 +944,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
   uint8_t* W = X + kTileB;
   uint8_t* S16 = X + 3 * kTileB;  // and the next chunk's rows of x
   const uint32_t sC = smem_u32(sm), sX = smem_u32(X), sW = smem_u32(W), sS = smem_u32(S16);
-  const int warp = __shfl_sync(0xffffffffu, pw, 0);  // the same for the whole warp
+  const int warp = pw;
   bool ok = true;
   int mmas = 0;
   float smax = 0.f;  // largest magnitude of this thread's part of S
@@ -958,13 +966,21 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
           prefetch_row(static_cast<const __nv_bfloat16*>(a.z) + t1 * a.H * a.P + s.c);
       }
       // ---- conv of X; the largest magnitude of S
-      wait_x();
-      float2 u[kTok];
-      const int eq = conv_x(taps, L, warp, lane, S16, halo, u, ex_s);
-      uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));
       const float4 w4 = ldgf4(gate + 4 * lane);
       const uint32_t eB4 = ldg32(ex + 4 * lane);
       const float w = ldgf(gate + warp * kTok + (lane & (kTok - 1)));
+      const float lfi = ldgf(gate + kL + i);
+      const int eBi = ldg8(ex + i);
+      const float4 bt = ldgf4(g.block + (chunk * a.H + s.h) * 4);
+      wait_x();
+      // u stays in the place of its two parts of wX until their scale is known (in registers
+      // beside S it would spill)
+      const int eq = conv_x(taps, L, warp, lane, S16, halo, ex_s, [&](int q, float2 u) {
+        const uint32_t at = pair_off(warp, lane, q);
+        *reinterpret_cast<float*>(W + at) = u.x;
+        *reinterpret_cast<float*>(W + at + kTileB) = u.y;
+      });
+      uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));
       if (lane == 0) top_s[warp] = top;
       if (bar_or_n(1 + pipe, kPipe, !ok)) break;
       // ---- S^ = fp16 operand of C S^T
@@ -989,18 +1005,20 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
         const int own = warp * kTok + (lane & (kTok - 1));
         const uint32_t e4 = __shfl_sync(0xffffffffu, eB4, own >> 2);
         const int eB = (int)(int8_t)(e4 >> (8 * (own & 3)));
-        store_wx(u, scale2(w, eB + kTargetW - wt), warp, lane, W);
-        const float xs = pow2(kTargetX - eq);
-        const uint32_t base = warp * kTok * 128 + ((lane >> 2) << 4) + (lane & 3) * 4;
+        const float wq = scale2(w, eB + kTargetW - wt), xs = pow2(kTargetX - eq);
 #pragma unroll
-        for (int q = 0; q < kTok; ++q)
-          *reinterpret_cast<uint32_t*>(X + (base ^ ((q & 7) << 4)) + q * 128) =
-              pack_f16x2(mul2(u[q], __shfl_sync(0xffffffffu, xs, q)));
+        for (int q = 0; q < kTok; ++q) {
+          const uint32_t at = pair_off(warp, lane, q);
+          const float2 u = make_float2(*reinterpret_cast<const float*>(W + at),
+                                       *reinterpret_cast<const float*>(W + at + kTileB));
+          *reinterpret_cast<uint32_t*>(X + at) =
+              pack_f16x2(mul2(u, __shfl_sync(0xffffffffu, xs, q)));
+          store_parts(u, __shfl_sync(0xffffffffu, wq, q), W, at);
+        }
       }
       // ---- g of token i, in units of its block's start
-      const float4 bt = ldgf4(g.block + (chunk * a.H + s.h) * 4);
       const int eX = ex_s[i];
-      const float gi = ldgf(gate + kL + i) + (float)(eX + ldg8(ex + i));
+      const float gi = lfi + (float)(eX + eBi);
       if (half == 0) {
         // its running maximum, and the maxima M of the blocks (lane l: tokens 4 l ..)
         const float4 lf4 = ldgf4(gate + kL + 4 * lane);
@@ -1155,16 +1173,27 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
       smax = 0.f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        float yi[8], yx[8];
+        float yi[8], yx[8], add[8];
         tmem_ld8(tmem_at(tI, quad * 32, p0 + 8 * r), yi);
         tmem_ld8(tmem_at(tX, quad * 32, p0 + 8 * r), yx);
+        tmem_ld8(tmem_at(tS, quad * 32, p0 + 8 * r), add);
         tmem_ld_wait();
+        // S^T <- 2^cum_L S^T + what the chunk adds
+#pragma unroll
+        for (int q = 0; q < 8; q += 2) {
+          const float2 n2 = __ffma2_rn(make_float2(dec, dec),
+                                       make_float2(sv[8 * r + q], sv[8 * r + q + 1]),
+                                       mul2(make_float2(add[q], add[q + 1]), ds));
+          sv[8 * r + q] = n2.x;
+          sv[8 * r + q + 1] = n2.y;
+          smax = fmaxf(smax, fmaxf(fabsf(n2.x), fabsf(n2.y)));
+        }
         if (in) {
           const uint4 xr = *reinterpret_cast<const uint4*>(X + sw128_off(i, half * 4 + r));
-          const uint32_t xw[4] = {xr.x, xr.y, xr.z, xr.w};
           const uint4 zv = zr[r & 1];
-          const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
           if (r < 2 && a.z) zr[r] = ldg128(zp + 8 * (r + 2));
+          const uint32_t xw[4] = {xr.x, xr.y, xr.z, xr.w};
+          const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
           uint32_t ow[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -1175,19 +1204,6 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
             ow[e] = pack_bf16x2(y.x, y.y);
           }
           *reinterpret_cast<uint4*>(op + 8 * r) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-        }
-        // ---- S^T <- 2^cum_L S^T + what the chunk adds
-        float add[8];
-        tmem_ld8(tmem_at(tS, quad * 32, p0 + 8 * r), add);
-        tmem_ld_wait();
-#pragma unroll
-        for (int q = 0; q < 8; q += 2) {
-          const float2 n2 = __ffma2_rn(make_float2(dec, dec),
-                                       make_float2(sv[8 * r + q], sv[8 * r + q + 1]),
-                                       mul2(make_float2(add[q], add[q + 1]), ds));
-          sv[8 * r + q] = n2.x;
-          sv[8 * r + q + 1] = n2.y;
-          smax = fmaxf(smax, fmaxf(fabsf(n2.x), fabsf(n2.y)));
         }
       }
       tc_fence_before();
