@@ -275,8 +275,8 @@ __device__ __forceinline__ Unit find_unit(const SsmArgs& a, int tokens, bool emp
 }
 
 // ------------------------------------------------------------------------------------- bc
-// 256 threads: warp w has tokens 16 w .. 16 w + 15 of the chunk, first of B, then of C; a lane
-// holds 4 channels of a row.  State widths below 128 are padded with zero channels.
+// 512 threads: warp w has tokens 8 w .. 8 w + 7 of the chunk, first of B, then of C; a lane holds 4
+// channels of a row.  State widths below 128 are padded with zero channels.
 constexpr uint32_t kBcSmem = 4 * kTileB + 2048;
 constexpr int kGateHeads = 32;  // heads per gates CTA
 
@@ -291,20 +291,20 @@ __device__ __forceinline__ void gates(const SsmTcArgs& g, const Unit& un, int pa
   {
     const int h = h0 + lane;
     const float bias = h < a.H && a.dt_bias ? a.dt_bias[h] : 0.f;
-    float raw[16];
+    float raw[8];
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int i = warp + 8 * q;
+    for (int q = 0; q < 8; ++q) {
+      const int i = warp + 16 * q;
       raw[q] = h < a.H && i < L ? __ldg(a.dt + (size_t)(t0 + i) * a.H + h) : 0.f;
     }
-#pragma unroll 4
-    for (int q = 0; q < 16; ++q) {
-      const int i = warp + 8 * q;
+#pragma unroll 1
+    for (int q = 0; q < 8; ++q) {
+      const int i = warp + 16 * q;
       d_s[lane * 132 + i] = h < a.H && i < L ? ssm_step(raw[q] + bias, a.dt_min, a.dt_max) : 0.f;
     }
   }
   __syncthreads();
-  for (int hh = warp; hh < kGateHeads; hh += 8) {
+  for (int hh = warp; hh < kGateHeads; hh += 16) {
     const int h = h0 + hh;
     if (h >= a.H) break;
     const float rate2 = -1.4426950408889634f * expf(a.a_log[h]);
@@ -347,10 +347,10 @@ __device__ __forceinline__ void gates(const SsmTcArgs& g, const Unit& un, int pa
   }
 }
 
-__global__ void __launch_bounds__(256, 2) ssm_bc_kernel(SsmTcArgs g) {
+__global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ SsmTcArgs g) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const SsmArgs& a = g.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   uint8_t* ctl = sm + 4 * kTileB;
   uint64_t* bar = reinterpret_cast<uint64_t*>(ctl);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(ctl + 8);
@@ -371,57 +371,55 @@ __global__ void __launch_bounds__(256, 2) ssm_bc_kernel(SsmTcArgs g) {
   const int t0 = un.s + un.j * kL, L = min(kL, un.e - t0);
   const size_t at = (size_t)(un.chunk + un.j) * a.G + grp;  // tile block
   const __nv_bfloat16* c0 = static_cast<const __nv_bfloat16*>(a.conv0);
-  const int row = state_row(a.slot, un.n, a.num_slots);
+  const int row = uniform(state_row(a.slot, un.n, a.num_slots));
   // the history the later kernels read: this group's share of the channels
   if (un.j == 0 && g.hist) {
     const int per = a.Cc / 8;
-    for (int v = grp * 256 + tid; v < 3 * per; v += a.G * 256) {
+    for (int v = grp * 512 + tid; v < 3 * per; v += a.G * 512) {
       uint4 r = make_uint4(0, 0, 0, 0);
       if (c0 && row >= 0) r = reinterpret_cast<const uint4*>(c0 + (size_t)row * 3 * a.Cc)[v];
       reinterpret_cast<uint4*>(g.hist + (size_t)un.n * 3 * a.Cc)[v] = r;
     }
   }
-  const int i0 = warp * 16;
+  const int i0 = warp * 8;
   uint8_t* tiles = g.tiles + at * kBcBytes;
   int8_t* ex = g.ex + at * 2 * kL;
   const bool live = lane * 4 < g.NS;
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {  // B, then C
     const int c = a.H * a.P + (part * a.G + grp) * g.NS + lane * 4;
+    uint2 raw[11];  // the warp's rows and the three before them
+#pragma unroll
+    for (int q = 0; q < 11; ++q) {  // (row addresses are the same for the whole warp)
+      const int t = t0 + i0 + q - 3;
+      const __nv_bfloat16* r =
+          t >= un.s ? static_cast<const __nv_bfloat16*>(a.x) + (size_t)t * a.Cc
+                    : (c0 && row >= 0 ? c0 + ((size_t)row * 3 + 3 + t - un.s) * a.Cc : nullptr);
+      raw[q] = make_uint2(0, 0);
+      if (r && i0 < L && t < un.e && live) raw[q] = *reinterpret_cast<const uint2*>(r + c);
+    }
+    uint4 wr[2] = {};
+    uint2 br = make_uint2(0, 0);
+    if (live) {
+      const __nv_bfloat16* cw = static_cast<const __nv_bfloat16*>(a.conv_w) + (size_t)c * 4;
+      wr[0] = __ldg(reinterpret_cast<const uint4*>(cw));
+      wr[1] = __ldg(reinterpret_cast<const uint4*>(cw + 8));
+      if (a.conv_b)
+        br = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.conv_b) + c));
+    }
     float2 w[4][2], b[2];  // taps and bias of the channel pairs
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      uint4 r = make_uint4(0, 0, 0, 0);
-      uint32_t rb = 0;
-      if (live) {
-        r = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.conv_w) +
-                                                 (size_t)(c + 2 * p) * 4));
-        if (a.conv_b)
-          rb = __ldg(reinterpret_cast<const uint32_t*>(
-              static_cast<const __nv_bfloat16*>(a.conv_b) + c + 2 * p));
-      }
-      const float2 wa = unpack_bf16x2(r.x), wb = unpack_bf16x2(r.y);
-      const float2 wc = unpack_bf16x2(r.z), wd = unpack_bf16x2(r.w);
+      const float2 wa = unpack_bf16x2(wr[p].x), wb = unpack_bf16x2(wr[p].y);
+      const float2 wc = unpack_bf16x2(wr[p].z), wd = unpack_bf16x2(wr[p].w);
       w[0][p] = make_float2(wa.x, wc.x), w[1][p] = make_float2(wa.y, wc.y);
       w[2][p] = make_float2(wb.x, wd.x), w[3][p] = make_float2(wb.y, wd.y);
-      b[p] = unpack_bf16x2(rb);
+      b[p] = unpack_bf16x2(p ? br.y : br.x);
     }
-    uint2 raw[19];
-    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + c;
+    uint32_t tops = 0;
+    uint8_t* hi_out = tiles + (part ? 0 : 2 * kTileB);
 #pragma unroll
-    for (int q = 0; q < 19; ++q) {
-      const int t = t0 + i0 + q - 3;
-      raw[q] = make_uint2(0, 0);
-      if (live && i0 < L && i0 + q - 3 < L) {
-        if (t >= un.s)
-          raw[q] = __ldg(reinterpret_cast<const uint2*>(x + (size_t)t * a.Cc));
-        else if (c0 && row >= 0)
-          raw[q] = *reinterpret_cast<const uint2*>(c0 + ((size_t)row * 3 + 3 + t - un.s) * a.Cc + c);
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int i = i0 + q;
+    for (int q = 0; q < 8; ++q) {
       float2 u[2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -430,22 +428,24 @@ __global__ void __launch_bounds__(256, 2) ssm_bc_kernel(SsmTcArgs g) {
         y = __ffma2_rn(w[1][p], word(raw[q + 1]), y);
         y = __ffma2_rn(w[2][p], word(raw[q + 2]), y);
         u[p] = silu2(__ffma2_rn(w[3][p], word(raw[q + 3]), y));
-        if (i >= L) u[p] = make_float2(0.f, 0.f);
+        if (i0 + q >= L) u[p] = make_float2(0.f, 0.f);
       }
       const uint32_t top = __reduce_max_sync(
-          0xffffffffu, max(max(abs_bits(u[0].x), abs_bits(u[0].y)),
-                           max(abs_bits(u[1].x), abs_bits(u[1].y))));
-      const int e2 = exponent_of(top);
-      if (lane == 0) ex[part * kL + i] = (int8_t)e2;
-      const float sc = pow2((part ? kTargetC : kTargetB) - e2);
+          0xffffffffu, __float_as_uint(fmaxf(fmaxf(fabsf(u[0].x), fabsf(u[0].y)),
+                                             fmaxf(fabsf(u[1].x), fabsf(u[1].y)))));
+      if (lane == q) tops = top;
+      const float sc = pow2((part ? kTargetC : kTargetB) - exponent_of(top));
       uint2 hi, lo;
       split2(mul2(u[0], sc), hi.x, lo.x);
       split2(mul2(u[1], sc), hi.y, lo.y);
-      const uint32_t off = (lane >> 4) * kTileB + sw128_off(i, (lane & 15) >> 1) + (lane & 1) * 8;
+      // row i0 + q of two row tiles (i0 is a multiple of 8: the swizzle goes by q)
+      const uint32_t off = ((lane >> 4) * kTileB + i0 * 128 + (((lane & 15) >> 1) << 4) +
+                            (lane & 1) * 8 ^ (q << 4)) + q * 128;
       *reinterpret_cast<uint2*>(sm + part * 2 * kTileB + off) = hi;
-      *reinterpret_cast<uint2*>(tiles + (part ? 0 : 2 * kTileB) + off) = hi;
-      if (!part) *reinterpret_cast<uint2*>(tiles + 4 * kTileB + off) = lo;
+      *reinterpret_cast<uint2*>(hi_out + off) = hi;
+      if (!part) *reinterpret_cast<uint2*>(hi_out + 2 * kTileB + off) = lo;
     }
+    if (lane < 8) ex[part * kL + i0 + lane] = (int8_t)exponent_of(tops);
   }
   fence_proxy_async_smem();
   __syncthreads();
@@ -460,13 +460,15 @@ __global__ void __launch_bounds__(256, 2) ssm_bc_kernel(SsmTcArgs g) {
     mma_commit(bar);
   }
   __syncwarp();
-  const bool ok = mbar_wait(bar, 0, g.wait_ns);
+  const bool ok = wait_long(bar, 0, g.wait_ns);
   tc_fence_after();
   if (!ok && tid == 0) report_status(a.status, GDN_ERR_TIMEOUT);
   // rows of the product: the blocks of 32 columns up to the diagonal
   const int i = (warp & 3) * 32 + lane;
   __half* cb = g.cb + (at * kL + i) * kL;
-  for (int blk = warp >> 2; blk <= (warp & 3); blk += 2) {
+  {
+    const int blk = warp >> 2;
+    if (blk <= (warp & 3)) {
     float v[32];
     tmem_ld32(tmem_at(tmem, (warp & 3) * 32, blk * 32), v);
     tmem_ld_wait();
@@ -479,11 +481,12 @@ __global__ void __launch_bounds__(256, 2) ssm_bc_kernel(SsmTcArgs g) {
       f.w = pack_f16x2(mul2(make_float2(v[8 * q + 6], v[8 * q + 7]), pow2(kScaleCB)));
       *reinterpret_cast<uint4*>(cb + blk * 32 + 8 * q) = f;
     }
+    }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
-    if (!ok) mbar_wait(bar, 0, g.wait_ns);  // the product still in flight
+    if (!ok) wait_long(bar, 0, g.wait_ns);  // the product still in flight
     tmem_dealloc(tmem, 128);
   }
 }
@@ -662,7 +665,7 @@ __device__ __forceinline__ void store_parts(float2 u, float w, uint8_t* W, uint3
 constexpr uint32_t kSegW = 8 * kTileB, kSegCtl = kSegW + 6 * kTileB;
 constexpr uint32_t kSegSmem = kSegCtl + 3072;
 
-__global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
+__global__ void __launch_bounds__(512, 1) ssm_seg_kernel(const __grid_constant__ SsmTcArgs g) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const SsmArgs& a = g.a;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -849,7 +852,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(SsmTcArgs g) {
 constexpr uint32_t kMainPipe = 6 * kTileB, kMainCtl = kMainPipe + 8 * kTileB;
 constexpr uint32_t kMainSmem = kMainCtl + 3072;
 
-__global__ void __launch_bounds__(512, 1) ssm_main_kernel(SsmTcArgs g) {
+__global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant__ SsmTcArgs g) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const SsmArgs& a = g.a;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -1333,7 +1336,7 @@ cudaError_t launch_ssm_tc(gdn::SsmTcArgs g, void* workspace, cudaStream_t s) {
                                          : gdn::kWaitLimitNs;
   const unsigned pairs = a.G * (((a.H / a.G) * (a.P / 64) + 1) / 2);
   const unsigned roles = a.G + (a.H + gdn::kGateHeads - 1) / gdn::kGateHeads;
-  cudaError_t e = launch_tc(false, gdn::ssm_bc_kernel, (unsigned)(a.T / gdn::kL + a.N) * roles, 256,
+  cudaError_t e = launch_tc(false, gdn::ssm_bc_kernel, (unsigned)(a.T / gdn::kL + a.N) * roles, 512,
                             gdn::kBcSmem, s, g, "ssm_bc");
   if (e == cudaSuccess && a.T > l.seg * gdn::kL)  // a sequence may have several segments
     e = launch_tc(true, gdn::ssm_seg_kernel, (unsigned)l.units * pairs, 512, gdn::kSegSmem, s, g,
