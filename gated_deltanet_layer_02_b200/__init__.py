@@ -581,6 +581,9 @@ def _arg(t, name, dtype, n, dev, required=False):
         if required:
             raise ValueError(f"{name} is required")
         return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.numel() >= n and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.numel() < n:
@@ -591,20 +594,19 @@ def _arg(t, name, dtype, n, dev, required=False):
         raise ValueError(f"{name} is on {t.device}; the call runs on cuda:{dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return t.data_ptr()
+    raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
 def _call_on(dev, name, *args):
     """One library call with device `dev` current, on that device's current stream."""
-    fn = getattr(lib(), name)
+    fn = getattr(_lib or lib(), name)
     if dev == torch.cuda.current_device():
-        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(name, code)
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if code:
+        raise GdnError(name, code)
 
 
 def ssm_conv_channels(dims: SsmDims) -> int:
@@ -616,13 +618,6 @@ def ssm_prefill_workspace_size(num_seqs: int, num_tokens: int, dtype=torch.bfloa
     return int(lib().gdn_ssm_prefill_workspace_size(
         ctypes.byref(dims or SsmDims()), GDN_BF16 if dtype == torch.bfloat16 else GDN_F32,
         num_seqs, num_tokens))
-
-
-def _cuda_index(t, name):
-    """Device of the call: that of its first tensor."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    return t.get_device()
 
 
 def _ssm_weights(dims, dt_x, dev, conv_w, conv_b, dt, dt_bias, a_log, D, T):
@@ -644,25 +639,26 @@ def ssm_prefill(x, dt, a_log, cu_seqlens, conv_w, conv_b=None, dt_bias=None, D=N
     D [H] fp32, conv_w [Cc, 4], conv_b [Cc], z [T, H, P] or None, cu_seqlens [N+1] int32 (device),
     S0 [N, H, P, state_dim] fp32 or None, conv0 [N, 3, Cc] or None.  Rows of out behind the last
     sequence (cu_seqlens[N] < T) are left as they were."""
+    lib()
     dims = dims or SsmDims()
     code, dtx, T, N = _act_dtype(x), x.dtype, x.shape[0], cu_seqlens.numel() - 1
     H, P, Ns, Cc = dims.num_heads, dims.head_dim, dims.state_dim, dims.channels
-    dev = _cuda_index(x, "x")
+    dev = x.get_device()
     px = _arg(x, "x", dtx, T * Cc, dev)
     w = _ssm_weights(dims, dtx, dev, conv_w, conv_b, dt, dt_bias, a_log, D, T)
     pz = _arg(z, "z", dtx, T * H * P, dev)
     pcu = _arg(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev)
-    if not x.is_cuda:
+    if dev < 0:
         raise ValueError("x must live on a CUDA device (no CPU fallback)")
     if out is None:
-        out = torch.empty((T, H, P), dtype=dtx, device=x.device)
+        out = x.new_empty((T, H, P))
     if want_state and SN is None:
-        SN = torch.empty((N, H, P, Ns), dtype=torch.float32, device=x.device)
+        SN = dt.new_empty((N, H, P, Ns))
     if want_state and convN is None:
-        convN = torch.empty((N, dims.conv_kernel - 1, Cc), dtype=dtx, device=x.device)
+        convN = x.new_empty((N, dims.conv_kernel - 1, Cc))
     if workspace is None:
-        workspace = torch.empty(ssm_prefill_workspace_size(N, T, dtx, dims), dtype=torch.uint8,
-                                device=x.device)
+        workspace = x.new_empty(_lib.gdn_ssm_prefill_workspace_size(ctypes.byref(dims), code, N, T),
+                                dtype=torch.uint8)
     n_s, n_c = N * H * P * Ns, N * (dims.conv_kernel - 1) * Cc
     _call_on(dev, "gdn_ssm_prefill", ctypes.byref(dims), code, px, *w, pz, pcu, N, T,
              _arg(S0, "S0", torch.float32, n_s, dev), _arg(SN, "SN", torch.float32, n_s, dev),
@@ -679,10 +675,11 @@ def ssm_prefill_slots(x, dt, a_log, cu_seqlens, S_pool, conv_w, slot_idx=None, c
     """ssm_prefill with the states in pools shared with ssm_decode_step: sequence n starts from and
     overwrites S_pool[slot_idx[n]] ([slots, H, P, state_dim] fp32) and conv_pool[slot_idx[n]]
     ([slots, 3, Cc]).  Slots as in chunk_prefill_slots.  Returns out [T, H, P]."""
+    lib()
     dims = dims or SsmDims()
     code, dtx, T, N = _act_dtype(x), x.dtype, x.shape[0], cu_seqlens.numel() - 1
     H, P = dims.num_heads, dims.head_dim
-    dev = _cuda_index(x, "x")
+    dev = x.get_device()
     px = _arg(x, "x", dtx, T * dims.channels, dev)
     w = _ssm_weights(dims, dtx, dev, conv_w, conv_b, dt, dt_bias, a_log, D, T)
     pz = _arg(z, "z", dtx, T * H * P, dev)
@@ -693,13 +690,13 @@ def ssm_prefill_slots(x, dt, a_log, cu_seqlens, S_pool, conv_w, slot_idx=None, c
     pslot = _arg(slot_idx, "slot_idx", torch.int32, N, dev)
     pS = _arg(S_pool, "S_pool", torch.float32, 0, dev, True)
     pc = _arg(conv_pool, "conv_pool", dtx, 0, dev)
-    if not x.is_cuda:
+    if dev < 0:
         raise ValueError("x must live on a CUDA device (no CPU fallback)")
     if out is None:
-        out = torch.empty((T, H, P), dtype=dtx, device=x.device)
+        out = x.new_empty((T, H, P))
     if workspace is None:
-        workspace = torch.empty(ssm_prefill_workspace_size(N, T, dtx, dims), dtype=torch.uint8,
-                                device=x.device)
+        workspace = x.new_empty(_lib.gdn_ssm_prefill_workspace_size(ctypes.byref(dims), code, N, T),
+                                dtype=torch.uint8)
     _call_on(dev, "gdn_ssm_prefill_slots", ctypes.byref(dims), code, px, *w, pz, pcu, N, T, pslot,
              rows, pS, pc, _arg(out, "out", dtx, T * H * P, dev),
              _arg(workspace, "workspace", torch.uint8, 0, dev), workspace.numel(),
@@ -721,10 +718,11 @@ def ssm_decode_step(x, dt, a_log, conv_state, S, conv_w, conv_b=None, dt_bias=No
     """One token per sequence; conv_state [slots, 3, Cc] and S [slots, H, P, state_dim] (fp32 or
     bf16) are updated in place.  Returns out [B, H, P].  A slot outside the pools is skipped on the
     device and reported in dev_status (GDN_ERR_INVALID_ARG)."""
+    lib()
     dims = dims or SsmDims()
     code, dtx, B = _act_dtype(x), x.dtype, x.shape[0]
     H, P, Cc = dims.num_heads, dims.head_dim, dims.channels
-    dev = _cuda_index(x, "x")
+    dev = x.get_device()
     px = _arg(x, "x", dtx, B * Cc, dev)
     w = _ssm_weights(dims, dtx, dev, conv_w, conv_b, dt, dt_bias, a_log, D, B)
     pz = _arg(z, "z", dtx, B * H * P, dev)
@@ -735,17 +733,19 @@ def ssm_decode_step(x, dt, a_log, conv_state, S, conv_w, conv_b=None, dt_bias=No
     pc = _arg(conv_state, "conv_state", dtx, 0, dev, True)
     bf16_state = S is not None and S.dtype == torch.bfloat16
     pS = _arg(S, "S", torch.bfloat16 if bf16_state else torch.float32, 0, dev, True)
-    if not x.is_cuda:
+    if dev < 0:
         raise ValueError("x must live on a CUDA device (no CPU fallback)")
     if out is None:
-        out = torch.empty((B, H, P), dtype=dtx, device=x.device)
-    if workspace is None:
-        workspace = torch.empty(lib().gdn_ssm_decode_workspace_size(ctypes.byref(dims), B),
-                                dtype=torch.uint8, device=x.device)
+        out = x.new_empty((B, H, P))
+    pw, nw = None, _lib.gdn_ssm_decode_workspace_size(ctypes.byref(dims), B)
+    if workspace is not None:
+        pw, nw = _arg(workspace, "workspace", torch.uint8, 0, dev), workspace.numel()
+    elif nw:
+        workspace = x.new_empty(nw, dtype=torch.uint8)
+        pw = workspace.data_ptr()
     _call_on(dev, "gdn_ssm_decode_step", ctypes.byref(dims), code,
              GDN_BF16 if bf16_state else GDN_F32, px, *w, pz, pc, pS, pslot, rows, B,
-             _arg(out, "out", dtx, B * H * P, dev),
-             _arg(workspace, "workspace", torch.uint8, 0, dev), workspace.numel(),
+             _arg(out, "out", dtx, B * H * P, dev), pw, nw,
              _arg(dev_status, "dev_status", torch.int32, 1, dev))
     return out
 
@@ -768,7 +768,7 @@ def batch_tables(ctx_lens, new_lens, slot_idx, page_table, free_pages, free_head
     to their rows, in place), free_pages [F] int32 of which those from free_head [1] on are free,
     num_rows >= the tokens of the step.  Returns a BatchTables; rows behind the last token hold -1.
     dev_status receives GDN_ERR_PAGES when the free list is too short (nothing is taken then)."""
-    dev = _cuda_index(new_lens, "new_lens")
+    dev = new_lens.get_device()
     N = new_lens.numel()
     pn = _arg(new_lens, "new_lens", torch.int32, 0, dev)
     pc = _arg(ctx_lens, "ctx_lens", torch.int32, N, dev)
@@ -781,13 +781,11 @@ def batch_tables(ctx_lens, new_lens, slot_idx, page_table, free_pages, free_head
     pt = _arg(page_table, "page_table", torch.int32, 0, dev)
     pf = _arg(free_pages, "free_pages", torch.int32, 0, dev, True)
     ph = _arg(free_head, "free_head", torch.int32, 1, dev, True)
-    if not new_lens.is_cuda:
+    if dev < 0:
         raise ValueError("new_lens must live on a CUDA device (no CPU fallback)")
     if out is None:
-        i32 = dict(dtype=torch.int32, device=new_lens.device)
-        out = BatchTables(torch.empty(N + 1, **i32), torch.empty(num_rows, **i32),
-                          torch.empty(num_rows, dtype=torch.int64, device=new_lens.device),
-                          torch.empty(1, **i32))
+        out = BatchTables(new_lens.new_empty(N + 1), new_lens.new_empty(num_rows),
+                          new_lens.new_empty(num_rows, dtype=torch.int64), new_lens.new_empty(1))
     _call_on(dev, "gdn_batch_tables", pc, pn, ps, slots, N, pt, width, pf, free_pages.numel(), ph,
              page_size, num_rows, _arg(out.cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev),
              _arg(out.positions, "positions", torch.int32, num_rows, dev),

@@ -102,7 +102,7 @@ struct PrefillArgs {
   float* carry_out;
 };
 
-// Selective state space layer: packed prefill (cu set) and one token per sequence (cu NULL).
+// Selective state space layer: packed prefill, and one token per sequence (N = T).
 struct SsmArgs {
   const void* x;         // [T][Cc] pre-conv rows [x | B | C]
   const void* conv_w;    // [Cc][4]
@@ -112,7 +112,7 @@ struct SsmArgs {
   const float* a_log;    // [H]
   const float* D;        // [H] or NULL
   const void* z;         // [T][H][P] or NULL
-  const int32_t* cu;     // [N+1], or NULL: sequence n is token n
+  const int32_t* cu;     // [N+1] (prompts)
   const void* S0;        // initial states, or NULL
   void* SN;              // final states, or NULL (may be S0)
   const void* conv0;
@@ -120,7 +120,7 @@ struct SsmArgs {
   void* out;
   const int32_t* slot;   // [N] state-pool rows, or NULL (= n)
   int32_t* status;
-  float* u;              // [T][Cc] conv outputs, fp32 (workspace)
+  float* u;              // workspace: [T][Cc] conv outputs, fp32
   int num_slots;
   int N, T, H, G, P, Cc;
   float dt_min, dt_max;

@@ -10,11 +10,6 @@ namespace gdn {
 // Tokens [s, e) of sequence n.  Entries of cu that are out of order or past T give an empty range
 // and GDN_ERR_INVALID_ARG.
 __device__ __forceinline__ void seq_range(const SsmArgs& a, int n, int& s, int& e) {
-  if (!a.cu) {
-    s = n;
-    e = n + 1;
-    return;
-  }
   s = __ldg(a.cu + n);
   e = __ldg(a.cu + n + 1);
   if (s < 0 || e < s || e > a.T) {

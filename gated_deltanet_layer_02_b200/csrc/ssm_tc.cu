@@ -1010,13 +1010,21 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
         const int eB = (int)(int8_t)(e4 >> (8 * (own & 3)));
         const float wq = scale2(w, eB + kTargetW - wt), xs = pow2(kTargetX - eq);
 #pragma unroll
-        for (int q = 0; q < kTok; ++q) {
-          const uint32_t at = pair_off(warp, lane, q);
-          const float2 u = make_float2(*reinterpret_cast<const float*>(W + at),
-                                       *reinterpret_cast<const float*>(W + at + kTileB));
-          *reinterpret_cast<uint32_t*>(X + at) =
-              pack_f16x2(mul2(u, __shfl_sync(0xffffffffu, xs, q)));
-          store_parts(u, __shfl_sync(0xffffffffu, wq, q), W, at);
+        for (int q0 = 0; q0 < kTok; q0 += 8) {  // eight loads, then their stores
+          float2 u[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t at = pair_off(warp, lane, q0 + q);
+            u[q] = make_float2(*reinterpret_cast<const float*>(W + at),
+                               *reinterpret_cast<const float*>(W + at + kTileB));
+          }
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t at = pair_off(warp, lane, q0 + q);
+            *reinterpret_cast<uint32_t*>(X + at) =
+                pack_f16x2(mul2(u[q], __shfl_sync(0xffffffffu, xs, q0 + q)));
+            store_parts(u[q], __shfl_sync(0xffffffffu, wq, q0 + q), W, at);
+          }
         }
       }
       // ---- g of token i, in units of its block's start

@@ -404,7 +404,8 @@ int gdn_ssm_prefill_slots(const gdn_ssm_dims* dims, gdn_dtype dtype, const void*
  *   GDN_BF16: read, updated in fp32 and rounded to nearest even once when written back);
  *   slot_idx [B] int32 nullable, num_slots, skipped slots, dev_status: as gdn_decode_step.
  *   workspace: at least gdn_ssm_decode_workspace_size() bytes, 256-byte aligned (the conv outputs
- *   of the step, fp32); calls that may overlap on the GPU need one each.
+ *   of the step, fp32); calls that may overlap on the GPU need one each.  Layers with up to 512
+ *   channels of x per group need none (size 0, NULL).
  */
 size_t gdn_ssm_decode_workspace_size(const gdn_ssm_dims* dims, int32_t batch);
 int gdn_ssm_decode_step(const gdn_ssm_dims* dims, gdn_dtype dtype, gdn_dtype state_dtype,

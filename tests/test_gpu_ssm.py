@@ -179,7 +179,7 @@ def test_bad_cu_seqlens_are_reported_and_read_nothing_outside():
 
 @pytest.mark.parametrize("state", [F32, BF], ids=["state32", "state16"])
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("shape", SHAPES + [(16, 1, 64, 128), (10, 2, 128, 64)], ids=str)
 def test_decode(shape, dtype, state):
     H, G, P, N = shape
     B, rows = 5, 9

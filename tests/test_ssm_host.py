@@ -33,7 +33,10 @@ def test_shapes(L):
     assert f(None, 1, 1, 100) == 0 and f(ref(), 1, -1, 5) == 0 and f(ref(), 4, 1, 5) == 0
     assert f(ref(head_dim=96), 1, 1, 100) == 0
     assert L.gdn_ssm_decode_workspace_size(ref(), -1) == 0
-    assert L.gdn_ssm_decode_workspace_size(ref(), 3) >= 3 * gdn.SsmDims().channels * 4
+    # up to 8 CTAs of 64 state rows per group are one cluster and need none
+    assert L.gdn_ssm_decode_workspace_size(ref(), 3) == 0
+    assert L.gdn_ssm_decode_workspace_size(ref(num_groups=4), 3) >= \
+        3 * gdn.SsmDims(num_groups=4).channels * 4
 
 
 def prefill(L, dims, dtype=1, x=A, w=A, b=None, dt=A, a_log=A, z=None, cu=A, N=1, T=16, S0=None,
@@ -76,7 +79,7 @@ def test_slots_refusals(L):
 
 
 def test_decode_refusals(L):
-    def call(dims=ref(), dtype=1, state=0, x=A, w=A, dt=A, a_log=A, conv=A, S=A, slot=A, slots=4,
+    def call(dims=ref(num_groups=1), dtype=1, state=0, x=A, w=A, dt=A, a_log=A, conv=A, S=A, slot=A, slots=4,
              B=2, out=A, ws=A, ws_bytes=1 << 40):
         return L.gdn_ssm_decode_step(dims, dtype, state, x, w, None, dt, None, a_log, None, None,
                                      conv, S, slot, slots, B, out, ws, ws_bytes, None, None)
