@@ -42,8 +42,7 @@ EXPORTS = (
     "gdn_block_prefill", "gdn_chunk_prefill_slots", "gdn_chunk_prefill_host_plan",
     "gdn_chunk_prefill_host_workspace_size", "gdn_chunk_prefill_host", "gdn_debug_set",
     "gdn_chunk_prefill_pages", "gdn_ssm_conv_channels", "gdn_ssm_prefill_workspace_size",
-    "gdn_ssm_prefill", "gdn_ssm_prefill_slots", "gdn_ssm_decode_workspace_size",
-    "gdn_ssm_decode_step", "gdn_batch_tables",
+    "gdn_ssm_prefill", "gdn_ssm_prefill_slots", "gdn_ssm_decode_step", "gdn_batch_tables",
 )
 
 #: size of the library-owned scratch used by chunk_prefill_static_ws (GDN_STATIC_WORKSPACE_BYTES)
@@ -165,10 +164,8 @@ def _configure(L):
                                   vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
     L.gdn_ssm_prefill_slots.argtypes = [sp, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32,
                                         i32, vp, i32, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
-    L.gdn_ssm_decode_workspace_size.argtypes = [sp, i32]
-    L.gdn_ssm_decode_workspace_size.restype = ctypes.c_size_t
     L.gdn_ssm_decode_step.argtypes = [sp, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp,
-                                      vp, vp, vp, vp, i32, i32, vp, vp, ctypes.c_size_t, vp, vp]
+                                      vp, vp, vp, vp, i32, i32, vp, vp, vp]
     L.gdn_batch_tables.argtypes = [vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, i32, i32, vp, vp,
                                    vp, vp, vp, vp]
     for name in EXPORTS:  # every declared symbol must resolve
@@ -713,8 +710,7 @@ def _ssm_pool_rows(S, conv_state, dims):
 
 
 def ssm_decode_step(x, dt, a_log, conv_state, S, conv_w, conv_b=None, dt_bias=None, D=None, z=None,
-                    slot_idx=None, out=None, workspace=None, dev_status=None,
-                    dims: SsmDims | None = None):
+                    slot_idx=None, out=None, dev_status=None, dims: SsmDims | None = None):
     """One token per sequence; conv_state [slots, 3, Cc] and S [slots, H, P, state_dim] (fp32 or
     bf16) are updated in place.  Returns out [B, H, P].  A slot outside the pools is skipped on the
     device and reported in dev_status (GDN_ERR_INVALID_ARG)."""
@@ -737,15 +733,9 @@ def ssm_decode_step(x, dt, a_log, conv_state, S, conv_w, conv_b=None, dt_bias=No
         raise ValueError("x must live on a CUDA device (no CPU fallback)")
     if out is None:
         out = x.new_empty((B, H, P))
-    pw, nw = None, _lib.gdn_ssm_decode_workspace_size(ctypes.byref(dims), B)
-    if workspace is not None:
-        pw, nw = _arg(workspace, "workspace", torch.uint8, 0, dev), workspace.numel()
-    elif nw:
-        workspace = x.new_empty(nw, dtype=torch.uint8)
-        pw = workspace.data_ptr()
     _call_on(dev, "gdn_ssm_decode_step", ctypes.byref(dims), code,
              GDN_BF16 if bf16_state else GDN_F32, px, *w, pz, pc, pS, pslot, rows, B,
-             _arg(out, "out", dtx, B * H * P, dev), pw, nw,
+             _arg(out, "out", dtx, B * H * P, dev),
              _arg(dev_status, "dev_status", torch.int32, 1, dev))
     return out
 

@@ -5,6 +5,7 @@
 // with bf16 activations run on the tensor cores (ssm_tc.cu).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <utility>
 
 #include "args.cuh"
@@ -66,32 +67,6 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(SsmArgs a) {
   }
 }
 
-// One token per sequence: a thread owns 8 channels of one sequence and shifts their history.
-template <typename T>
-__global__ void __launch_bounds__(128) ssm_conv_step_kernel(SsmArgs a) {
-  pdl_trigger();
-  const int c = (blockIdx.x * 128 + threadIdx.x) * 8, n = blockIdx.y;
-  if (c >= a.Cc) return;
-  const int row = state_row(a.slot, n, a.num_slots);
-  if (row < 0) {  // slot out of range: the sequence is skipped
-    if (c == 0) report_status(a.status, GDN_ERR_INVALID_ARG);
-    return;
-  }
-  float w[4][8], b[8], h[4][8], out[8];
-  T* cs = static_cast<T*>(a.convN) + (size_t)row * 3 * a.Cc + c;
-#pragma unroll
-  for (int j = 0; j < 3; ++j) load8(cs + (size_t)j * a.Cc, h[j]);
-  load8(static_cast<const T*>(a.x) + (size_t)n * a.Cc + c, h[3]);
-  load_taps<T>(a, c, w, b);
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    out[e] = silu_f(fmaf(w[3][e], h[3][e],
-                         fmaf(w[2][e], h[2][e], fmaf(w[1][e], h[1][e], fmaf(w[0][e], h[0][e], b[e])))));
-#pragma unroll
-  for (int j = 0; j < 3; ++j) store8(cs + (size_t)j * a.Cc, h[j + 1]);
-  store8(a.u + (size_t)n * a.Cc + c, out);
-}
-
 // Four consecutive elements of an activation row (8 or 16 bytes).
 __device__ __forceinline__ void load_t4(const float* p, float (&v)[4]) {
   const float4 r = *reinterpret_cast<const float4*>(p);
@@ -110,99 +85,83 @@ __device__ __forceinline__ void store_t4(__nv_bfloat16* p, const float (&v)[4]) 
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-// Four consecutive elements of a state row.
-__device__ __forceinline__ float4 load4(const float* p) {
-  return __ldcs(reinterpret_cast<const float4*>(p));
-}
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 r = __ldcs(reinterpret_cast<const uint2*>(p));
-  const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.x));
-  const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.y));
-  return make_float4(lo.x, lo.y, hi.x, hi.y);
-}
-__device__ __forceinline__ void store4(float* p, float4 v) {
-  __stcs(reinterpret_cast<float4*>(p), v);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)));
-}
-
-// Lane `sub` of a row's eight lanes holds columns 4 sub + 32 m + e (m < NS / 32).  Warp w owns
-// rows 16 w + 4 q + lane / 8 (q < 4) of the CTA's 64.
-template <typename TS, int NS>
-struct StateRows {
-  static constexpr int M = NS / 32;
-  float4 f[4][M];
-  __device__ __forceinline__ void load(const TS* p) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int m = 0; m < M; ++m)
-        f[q][m] = p ? load4(p + (size_t)(4 * q) * NS + 32 * m) : make_float4(0.f, 0.f, 0.f, 0.f);
+// State rows in registers: lane `sub` of a row's eight lanes holds columns 4 sub + 32 m + e
+// (m < NS / 32).  A quad is four rows, one per group of eight lanes.
+//
+// Raw: four elements as they are stored, so that loads stay in flight in as few registers as they
+// have bytes.
+template <typename TS>
+struct Raw;
+template <>
+struct Raw<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = __ldcs(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ float4 get() const { return v; }
+  static __device__ __forceinline__ void store(float* p, float4 r) {
+    __stcs(reinterpret_cast<float4*>(p), r);
   }
-  __device__ __forceinline__ void store(TS* p) const {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int m = 0; m < M; ++m) store4(p + (size_t)(4 * q) * NS + 32 * m, f[q][m]);
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    v = __ldcs(reinterpret_cast<const uint2*>(p));
   }
-  // One token: the rows take alpha S + (delta x) B^T; returns S C of row q in every lane of its
-  // group of eight.  B, C: the lane's first column.
-  __device__ __forceinline__ void step(const float* B, const float* C, const float (&dx)[4],
-                                       float alpha, float (&o)[4]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) o[q] = 0.f;
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const float4 b = *reinterpret_cast<const float4*>(B + 32 * m);
-      const float4 c = *reinterpret_cast<const float4*>(C + 32 * m);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float4& r = f[q][m];
-        r.x = fmaf(alpha, r.x, dx[q] * b.x);
-        r.y = fmaf(alpha, r.y, dx[q] * b.y);
-        r.z = fmaf(alpha, r.z, dx[q] * b.z);
-        r.w = fmaf(alpha, r.w, dx[q] * b.w);
-        o[q] = fmaf(r.x, c.x, fmaf(r.y, c.y, fmaf(r.z, c.z, fmaf(r.w, c.w, o[q]))));
-      }
-    }
-#pragma unroll
-    for (int off = 4; off > 0; off >>= 1)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) o[q] += __shfl_xor_sync(0xffffffffu, o[q], off);
+  __device__ __forceinline__ float4 get() const {
+    const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
+    const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, float4 r) {
+    __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack_bf16x2(r.x, r.y), pack_bf16x2(r.z, r.w)));
   }
 };
 
-// Lane `sub` < 4 of a group writes its row 4 sub: y = S C + D x, gated.
-template <typename T>
-__device__ __forceinline__ void store_y(const SsmArgs& a, int t, int h, int p0, int sub, float D,
-                                        const float (&xv)[4], const float (&o)[4]) {
-  if (sub < 4) {
-    const float y0 = sub == 0 ? o[0] : (sub == 1 ? o[1] : (sub == 2 ? o[2] : o[3]));
-    const float x0 = sub == 0 ? xv[0] : (sub == 1 ? xv[1] : (sub == 2 ? xv[2] : xv[3]));
-    float y = fmaf(D, x0, y0);
-    const size_t at = ((size_t)t * a.H + h) * a.P + p0 + 4 * sub;
-    if (a.z) y *= silu_f(to_f(static_cast<const T*>(a.z)[at]));
-    static_cast<T*>(a.out)[at] = from_f<T>(y);
+// One token of Q quads: the rows take alpha S + dx B^T; o: S C of the lane's row of each quad, in
+// every lane of its group of eight.  B, C: the lane's first column.
+template <int Q, int M>
+__device__ __forceinline__ void ssm_rows_step(float4 (&f)[Q][M], const float* B, const float* C,
+                                              const float (&dx)[Q], float alpha, float (&o)[Q]) {
+#pragma unroll
+  for (int q = 0; q < Q; ++q) o[q] = 0.f;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const float4 b = *reinterpret_cast<const float4*>(B + 32 * m);
+    const float4 c = *reinterpret_cast<const float4*>(C + 32 * m);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float4& r = f[q][m];
+      r.x = fmaf(alpha, r.x, dx[q] * b.x);
+      r.y = fmaf(alpha, r.y, dx[q] * b.y);
+      r.z = fmaf(alpha, r.z, dx[q] * b.z);
+      r.w = fmaf(alpha, r.w, dx[q] * b.w);
+      o[q] = fmaf(r.x, c.x, fmaf(r.y, c.y, fmaf(r.z, c.z, fmaf(r.w, c.w, o[q]))));
+    }
   }
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1)
+#pragma unroll
+    for (int q = 0; q < Q; ++q) o[q] += __shfl_xor_sync(0xffffffffu, o[q], off);
 }
 
 // ------------------------------------------------------------------------- packed prompts, fp32
-// Tokens of a sequence come kScanBlock at a time to shared memory (B, C, the CTA's 64 channels of x,
-// step and decay), the next ones in flight while these are worked through.
+// Tokens of a sequence come kScanBlock at a time to shared memory (B, C, the CTA's channels of x and
+// z, step and decay), the next ones in flight while these are worked through; y takes the place of
+// x and leaves a block at a time.  A CTA has 16 Q rows of a head's state, 4 Q per warp.
 constexpr int kScanBlock = 16;
-template <int NS>
+template <int NS, int Q>
 struct ScanTokens {
-  float B[kScanBlock][NS], C[kScanBlock][NS], x[kScanBlock][kScanRows];
+  float B[kScanBlock][NS], C[kScanBlock][NS], x[kScanBlock][16 * Q], z[kScanBlock][16 * Q];
   float2 gate[kScanBlock];  // step, decay
 };
 
-template <int NS>
+template <int NS, int Q>
 __global__ void __launch_bounds__(kScanThreads, 4) ssm_scan_kernel(SsmArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  ScanTokens<NS>* buf = reinterpret_cast<ScanTokens<NS>*>(smem);  // [2]
-  pdl_trigger();
-  const int blocks = a.P / kScanRows;
+  using Tokens = ScanTokens<NS, Q>;
+  constexpr int kRows = 16 * Q, M = NS / 32;
+  Tokens* buf = reinterpret_cast<Tokens*>(smem);  // [2]
+  const int blocks = a.P / kRows;
   const int pb = blockIdx.x % blocks, h = (blockIdx.x / blocks) % a.H;
   const int n = blockIdx.x / (blocks * a.H);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grp = lane >> 3, sub = lane & 7;
@@ -210,27 +169,47 @@ __global__ void __launch_bounds__(kScanThreads, 4) ssm_scan_kernel(SsmArgs a) {
   if (row < 0 && tid == 0) report_status(a.status, GDN_ERR_INVALID_ARG);
   int s, end;
   seq_range(a, n, s, end);
-  const int p0 = pb * kScanRows + warp * 16 + grp;  // this lane group's rows: p0 + 4 q
+  const int r0 = warp * 4 * Q + grp, p0 = pb * kRows + r0;  // this lane group's rows: p0 + 4 q
   const size_t sbase = (((size_t)(row < 0 ? 0 : row) * a.H + h) * a.P + p0) * NS + 4 * sub;
-  StateRows<float, NS> S;
-  S.load(a.S0 && row >= 0 ? static_cast<const float*>(a.S0) + sbase : nullptr);
+  float4 f[Q][M];
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+      f[q][m] = a.S0 && row >= 0
+                    ? __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(a.S0) + sbase +
+                                                             (size_t)(4 * q) * NS + 32 * m))
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
   const float rate = -expf(a.a_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   const float D = a.D ? a.D[h] : 0.f;
   const int cB = a.H * a.P + (h / (a.H / a.G)) * NS, cC = cB + a.G * NS;
-  const int cx = h * a.P + pb * kScanRows;
-  // 16-byte pieces of a token: NS / 4 of B, as many of C, 16 of x
-  auto fetch = [&](int t0, ScanTokens<NS>& b) {
-    constexpr int kPieces = NS / 2 + kScanRows / 4;
+  const int cx = h * a.P + pb * kRows;
+  // 16-byte pieces of a token: NS / 4 of B, as many of C, 4 Q of x, 4 Q of z
+  auto fetch = [&](int t0, Tokens& b) {
+    constexpr int kBC = NS / 4, kX = kRows / 4, kPieces = 2 * kBC + 2 * kX;
     for (int v = tid; v < kScanBlock * kPieces; v += kScanThreads) {
       const int t = v / kPieces, p = v % kPieces;
-      const int c = p < NS / 4 ? cB + 4 * p
-                               : (p < NS / 2 ? cC + 4 * p - NS : cx + 4 * p - 2 * NS);
-      float* dst = p < NS / 4 ? &b.B[t][4 * p]
-                              : (p < NS / 2 ? &b.C[t][4 * p - NS] : &b.x[t][4 * p - 2 * NS]);
-      if (t0 + t < end)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
-                     "l"(a.u + (size_t)(t0 + t) * a.Cc + c)
-                     : "memory");
+      if (t0 + t >= end) break;
+      const float* u = a.u + (size_t)(t0 + t) * a.Cc;
+      const float* src;
+      float* dst;
+      if (p < kBC) {
+        src = u + cB + 4 * p;
+        dst = &b.B[t][4 * p];
+      } else if (p < 2 * kBC) {
+        src = u + cC + 4 * (p - kBC);
+        dst = &b.C[t][4 * (p - kBC)];
+      } else if (p < 2 * kBC + kX) {
+        src = u + cx + 4 * (p - 2 * kBC);
+        dst = &b.x[t][4 * (p - 2 * kBC)];
+      } else {
+        if (!a.z) continue;
+        src = static_cast<const float*>(a.z) + (size_t)(t0 + t) * a.H * a.P + cx +
+              4 * (p - 2 * kBC - kX);
+        dst = &b.z[t][4 * (p - 2 * kBC - kX)];
+      }
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                   : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (tid < kScanBlock && t0 + tid < end) {
@@ -248,115 +227,182 @@ __global__ void __launch_bounds__(kScanThreads, 4) ssm_scan_kernel(SsmArgs a) {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     __syncthreads();
-    const ScanTokens<NS>& b = buf[k];
+    Tokens& b = buf[k];
     const int m = min(kScanBlock, end - t0);
 #pragma unroll 2
     for (int i = 0; i < m; ++i) {
-      float xv[4], dx[4], o[4];
+      float xv[Q], dx[Q], o[Q];
       const float2 gt = b.gate[i];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        xv[q] = b.x[i][warp * 16 + grp + 4 * q];
+      for (int q = 0; q < Q; ++q) {
+        xv[q] = b.x[i][r0 + 4 * q];
         dx[q] = gt.x * xv[q];
       }
-      S.step(&b.B[i][4 * sub], &b.C[i][4 * sub], dx, gt.y, o);
-      store_y<float>(a, t0 + i, h, p0, sub, D, xv, o);
+      ssm_rows_step(f, &b.B[i][4 * sub], &b.C[i][4 * sub], dx, gt.y, o);
+      if (sub == 0) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) b.x[i][r0 + 4 * q] = fmaf(D, xv[q], o[q]);
+      }
+    }
+    __syncthreads();
+    for (int v = tid; v < m * (kRows / 4); v += kScanThreads) {
+      const int t = v / (kRows / 4), p = 4 * (v % (kRows / 4));
+      float4 y = *reinterpret_cast<const float4*>(&b.x[t][p]);
+      if (a.z) {
+        const float4 z = *reinterpret_cast<const float4*>(&b.z[t][p]);
+        y.x *= silu_f(z.x), y.y *= silu_f(z.y), y.z *= silu_f(z.z), y.w *= silu_f(z.w);
+      }
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (size_t)(t0 + t) * a.H * a.P + cx + p) = y;
     }
     __syncthreads();  // the buffer takes the tokens after the next ones
   }
   conv_history<float>(a, n, row, s, end, blockIdx.x % (blocks * a.H), blocks * a.H);
-  if (a.SN && row >= 0) S.store(static_cast<float*>(a.SN) + sbase);
+  if (a.SN && row >= 0) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        __stcs(reinterpret_cast<float4*>(static_cast<float*>(a.SN) + sbase + (size_t)(4 * q) * NS +
+                                         32 * m),
+               f[q][m]);
+  }
 }
 
 // ------------------------------------------------------------------------------- single tokens
-// One token per sequence: the rows of the state are on their way before the conv.
-//   FUSED: the CTAs of a group of heads are one cluster.  Each computes the conv of its own 64
-//   channels of x and of the group's B and C (a few KB beside 64 KB of state in and out), and
-//   shifts the history of its x; that of B and C is shifted, split over the cluster, when all of
-//   it has been read.  One launch and no workspace: 256 sequences of 32 heads of 128 x 128 take
-//   the state's bytes; one sequence the latency of one launch.
-//   Else (more than 8 CTAs share B and C): the conv outputs come from ssm_conv_step_kernel.
-template <typename T, typename TS, int NS, bool FUSED>
-__global__ void __launch_bounds__(kScanThreads, 4) ssm_step_kernel(SsmArgs a) {
-  __shared__ __align__(16) float u_s[kScanRows + 2 * NS];  // x | B | C
-  const int blocks = a.P / kScanRows, per = a.H / a.G;
-  const int pb = blockIdx.x % blocks, h = (blockIdx.x / blocks) % a.H;
-  const int n = blockIdx.x / (blocks * a.H), g = h / per;
+// One token per sequence.  A group of heads (which share B and C) is worked on by a cluster of `cl`
+// CTAs, each with `nb` blocks of 64 state rows one after the other: every warp streams its rows in
+// batches, the next batch in flight while one is updated, the first on its way before the conv.
+// Every CTA computes the conv of its own channels of x and, again, of the group's B and C (a few KB
+// beside 32 KB of state in and out per block); it shifts the history of its x, and that of B and C
+// is shifted, split over the cluster, when all of it has been read.  So it is one launch without a
+// workspace, from one sequence (cl = 8: all the parallelism there is) to many (cl = 1).
+template <typename T, typename TS, int NS>
+__global__ void __launch_bounds__(kScanThreads, 4) ssm_step_kernel(SsmArgs a, int cl, int nb) {
+  constexpr int M = NS / 32, Q = sizeof(TS) == 4 ? 2 : 4;  // quads per batch of a warp
+  constexpr int kBatches = 4 / Q;                          // batches of a block of 64 rows
+  extern __shared__ __align__(16) float st_s[];
+  const int blocks = a.P / kScanRows, per = a.H / a.G, R = per * blocks;
+  const int rank = blockIdx.x % cl, g = (blockIdx.x / cl) % a.G, n = blockIdx.x / (cl * a.G);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grp = lane >> 3, sub = lane & 7;
   const int row = state_row(a.slot, n, a.num_slots);
   if (row < 0) {  // slot out of range: the sequence is skipped (by its whole clusters)
-    if (tid == 0) report_status(a.status, GDN_ERR_INVALID_ARG);
-    if (!FUSED) pdl_wait();
+    if (tid == 0 && rank == 0) report_status(a.status, GDN_ERR_INVALID_ARG);
     return;
   }
-  const int p0 = pb * kScanRows + warp * 16 + grp;
-  const size_t sbase = (((size_t)row * a.H + h) * a.P + p0) * NS + 4 * sub;
-  StateRows<TS, NS> S;
-  S.load(static_cast<const TS*>(a.S0) + sbase);
-  const float bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
-  const float delta = ssm_step(a.dt[(size_t)n * a.H + h] + bias, a.dt_min, a.dt_max);
-  const float alpha = expf(-expf(a.a_log[h]) * delta);
-  const int cx = h * a.P + pb * kScanRows, cB = a.H * a.P + g * NS, cC = cB + a.G * NS;
-  constexpr int kItems = (kScanRows + 2 * NS) / 4;  // of 4 channels, one per thread
-  const int rank = (h % per) * blocks + pb, ranks = per * blocks;
-  const int c = tid < kScanRows / 4 ? cx + 4 * tid
-                                    : (tid < (kScanRows + NS) / 4 ? cB + 4 * tid - kScanRows
-                                                                  : cC + 4 * tid - kScanRows - NS);
-  if (FUSED) {
-    float v[4][4], w[4][4], b[4] = {0.f, 0.f, 0.f, 0.f};
-    T* cs = static_cast<T*>(a.convN) + (size_t)row * 3 * a.Cc + c;
-    if (tid < kItems) {
+  const int b0 = rank * nb, mine = max(0, min(nb, R - b0));  // blocks b0 .. of the group
+  float* B_s = st_s;                          // [NS]
+  float* C_s = B_s + NS;                      // [NS]
+  float* x_s = C_s + NS;                      // [64 nb] conv outputs, then y
+  float2* gate_s = reinterpret_cast<float2*>(x_s + kScanRows * nb);  // [nb] decay, step of a block's head
+  const int c0 = g * per * a.P + b0 * kScanRows;  // first channel of x (and of the output)
+  TS* S = static_cast<TS*>(a.SN) + ((size_t)row * a.H * a.P + c0 + warp * 16 + grp) * NS + 4 * sub;
+  auto load = [&](int bt, Raw<TS> (&r)[Q][M]) {  // batch bt of this warp's rows
+    const TS* p = S + ((size_t)(bt / kBatches) * kScanRows + (bt % kBatches) * (4 * Q)) * NS;
 #pragma unroll
-      for (int j = 0; j < 3; ++j) load_t4(cs + (size_t)j * a.Cc, v[j]);
-      load_t4(static_cast<const T*>(a.x) + (size_t)n * a.Cc + c, v[3]);
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) load_t4(static_cast<const T*>(a.conv_w) + (size_t)(c + e) * 4, w[e]);
-      if (a.conv_b) load_t4(static_cast<const T*>(a.conv_b) + c, b);
-      float4 u;
-      float* up = &u.x;
+      for (int m = 0; m < M; ++m) r[q][m].load(p + (size_t)(4 * q) * NS + 32 * m);
+  };
+  Raw<TS> cur[Q][M], nxt[Q][M];
+  if (mine > 0) load(0, cur);
+  for (int b = tid; b < mine; b += kScanThreads) {
+    const int h = g * per + (b0 + b) / blocks;
+    const float d = ssm_step(a.dt[(size_t)n * a.H + h] + (a.dt_bias ? a.dt_bias[h] : 0.f), a.dt_min,
+                             a.dt_max);
+    gate_s[b] = make_float2(expf(-expf(a.a_log[h]) * d), d);
+  }
+  // ---- conv + SiLU, 4 channels per item: B, C, then this CTA's x
+  const int cB = a.H * a.P + g * NS;
+  T* hist = static_cast<T*>(a.convN) + (size_t)row * 3 * a.Cc;
+  auto conv = [&](int c, float* u, float (&v)[4][4]) {
+    float w[4][4], b[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        up[e] = silu_f(fmaf(w[e][3], v[3][e],
-                            fmaf(w[e][2], v[2][e], fmaf(w[e][1], v[1][e], fmaf(w[e][0], v[0][e], b[e])))));
-      *reinterpret_cast<float4*>(u_s + 4 * tid) = u;
-    }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // has read the history
-    const bool x_part = tid < kScanRows / 4;
-    if (tid < kItems && x_part) {
+    for (int j = 0; j < 3; ++j) load_t4(hist + (size_t)j * a.Cc + c, v[j]);
+    load_t4(static_cast<const T*>(a.x) + (size_t)n * a.Cc + c, v[3]);
 #pragma unroll
-      for (int j = 0; j < 3; ++j) store_t4(cs + (size_t)j * a.Cc, v[j + 1]);
+    for (int e = 0; e < 4; ++e) load_t4(static_cast<const T*>(a.conv_w) + (size_t)(c + e) * 4, w[e]);
+    if (a.conv_b) load_t4(static_cast<const T*>(a.conv_b) + c, b);
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      y[e] = silu_f(fmaf(w[e][3], v[3][e],
+                         fmaf(w[e][2], v[2][e], fmaf(w[e][1], v[1][e], fmaf(w[e][0], v[0][e], b[e])))));
+    *reinterpret_cast<float4*>(u) = make_float4(y[0], y[1], y[2], y[3]);
+  };
+  auto shift = [&](int c, const float (&v)[4][4]) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) store_t4(hist + (size_t)j * a.Cc + c, v[j + 1]);
+  };
+  static_assert(2 * NS / 4 <= kScanThreads, "an item of B or C per thread");
+  {
+    const int cbc = tid < NS / 4 ? cB + 4 * tid : cB + (a.G - 1) * NS + 4 * tid;
+    float v[4][4];
+    const bool bc = tid < 2 * NS / 4;
+    if (bc) conv(cbc, B_s + 4 * tid, v);
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // has read B's and C's
+    for (int it = tid; it < mine * (kScanRows / 4); it += kScanThreads) {
+      float vx[4][4];
+      conv(c0 + 4 * it, x_s + 4 * it, vx);
+      shift(c0 + 4 * it, vx);
     }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (tid < kItems && !x_part && tid % ranks == rank) {
+    if (bc && tid % cl == rank) shift(cbc, v);
+  }
+  __syncthreads();
+
+  // ---- the state
+  for (int bt = 0; bt < mine * kBatches; ++bt) {
+    if (bt + 1 < mine * kBatches) load(bt + 1, nxt);
+    const int b = bt / kBatches, r0 = warp * 16 + (bt % kBatches) * (4 * Q) + grp;
+    const float2 gt = gate_s[b];
+    float4 f[Q][M];
+    float xv[Q], dx[Q], o[Q];
 #pragma unroll
-      for (int j = 0; j < 3; ++j) store_t4(cs + (size_t)j * a.Cc, v[j + 1]);
+    for (int q = 0; q < Q; ++q) {
+      xv[q] = x_s[b * kScanRows + r0 + 4 * q];
+      dx[q] = gt.y * xv[q];
+#pragma unroll
+      for (int m = 0; m < M; ++m) f[q][m] = cur[q][m].get();
     }
-    __syncthreads();
-  } else {
-    pdl_wait();  // the conv outputs
-    if (tid < kItems)
-      *reinterpret_cast<float4*>(u_s + 4 * tid) =
-          *reinterpret_cast<const float4*>(a.u + (size_t)n * a.Cc + c);
-    __syncthreads();
-  }
-  float xv[4], dx[4], o[4];
+    ssm_rows_step(f, B_s + 4 * sub, C_s + 4 * sub, dx, gt.x, o);
+    TS* p = S + ((size_t)b * kScanRows + (bt % kBatches) * (4 * Q)) * NS;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    xv[q] = u_s[warp * 16 + grp + 4 * q];
-    dx[q] = delta * xv[q];
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int m = 0; m < M; ++m) Raw<TS>::store(p + (size_t)(4 * q) * NS + 32 * m, f[q][m]);
+    if (sub == 0) {  // y takes the place of x (read by this group of lanes alone)
+      const float D = a.D ? a.D[g * per + (b0 + b) / blocks] : 0.f;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) x_s[b * kScanRows + r0 + 4 * q] = fmaf(D, xv[q], o[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int m = 0; m < M; ++m) cur[q][m] = nxt[q][m];
   }
-  S.step(u_s + kScanRows + 4 * sub, u_s + kScanRows + NS + 4 * sub, dx, alpha, o);
-  S.store(static_cast<TS*>(a.SN) + sbase);
-  store_y<T>(a, n, h, p0, sub, D, xv, o);
+  __syncthreads();
+  // ---- outputs
+  for (int it = tid; it < mine * (kScanRows / 4); it += kScanThreads) {
+    const size_t at = (size_t)n * a.H * a.P + c0 + 4 * it;
+    float y[4];
+    load_t4(x_s + 4 * it, y);
+    if (a.z) {
+      float z[4];
+      load_t4(static_cast<const T*>(a.z) + at, z);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] *= silu_f(z[e]);
+    }
+    store_t4(static_cast<T*>(a.out) + at, y);
+  }
 }
 
 }  // namespace gdn
 
 namespace gdn_host {
 
-template <typename K>
-static cudaError_t launch_ssm(bool pdl, int cluster, K kern, dim3 grid, size_t smem, cudaStream_t s,
-                              const gdn::SsmArgs& a, const char* name) {
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_ssm(const char* name, bool pdl, int cluster, void (*kern)(KArgs...),
+                              dim3 grid, size_t smem, cudaStream_t s, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(128);
@@ -377,13 +423,26 @@ static cudaError_t launch_ssm(bool pdl, int cluster, K kern, dim3 grid, size_t s
   cfg.attrs = attr;
   cfg.numAttrs = n;
   trace_begin(name, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
   trace_end(s);
   return e;
 }
 
 cudaError_t launch_ssm_tc(gdn::SsmTcArgs g, void* workspace, cudaStream_t s);
 size_t ssm_tc_workspace(int N, int T, int H, int G, int P, int NS, int Cc);
+
+template <int NS, int Q>
+static cudaError_t launch_scan(const gdn::SsmArgs& a, cudaStream_t s) {
+  const bool pdl = a.T > 0;  // behind a conv of this call; alone, it is an ordinary launch
+  const size_t smem = 2 * sizeof(gdn::ScanTokens<NS, Q>);
+  if (smem > 48 * 1024) {  // per call, not once: the attribute belongs to the current device
+    const cudaError_t e = cudaFuncSetAttribute(
+        gdn::ssm_scan_kernel<NS, Q>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_ssm("ssm_scan", pdl, 1, gdn::ssm_scan_kernel<NS, Q>,
+                    dim3((unsigned)a.N * a.H * (a.P / (16 * Q))), smem, s, a);
+}
 
 static cudaError_t launch_ssm_prefill(bool bf16, const gdn::SsmArgs& a, int NS, cudaStream_t s) {
   if (bf16) {
@@ -394,49 +453,53 @@ static cudaError_t launch_ssm_prefill(bool bf16, const gdn::SsmArgs& a, int NS, 
   }
   if (a.T > 0) {
     const dim3 grid((a.T + gdn::kConvRun - 1) / gdn::kConvRun, (a.Cc / 8 + 127) / 128);
-    cudaError_t e = launch_ssm(false, 1, gdn::ssm_conv_kernel<float>, grid, 0, s, a, "ssm_conv");
+    cudaError_t e = launch_ssm("ssm_conv", false, 1, gdn::ssm_conv_kernel<float>, grid, 0, s, a);
     if (e != cudaSuccess) return e;
   }
-  const bool pdl = a.T > 0;  // behind a conv of this call; alone, it is an ordinary launch
-  const dim3 grid((unsigned)a.N * a.H * (a.P / gdn::kScanRows));
-  const size_t smem = 2 * (NS == 128 ? sizeof(gdn::ScanTokens<128>) : sizeof(gdn::ScanTokens<64>));
-  return NS == 128
-             ? launch_ssm(pdl, 1, gdn::ssm_scan_kernel<128>, grid, smem, s, a, "ssm_scan")
-             : launch_ssm(pdl, 1, gdn::ssm_scan_kernel<64>, grid, smem, s, a, "ssm_scan");
+  // Rows per CTA: 16 where that is needed to have work for all SMs (a token costs one quad per warp
+  // and not four: 1000 tokens of two sequences of 64 heads of 64 x 128 take 350 us and not 525), 64
+  // else (B and C are read for four quads at once: eight such sequences 178 us and not 243).
+  if ((int64_t)a.N * a.H * (a.P / 64) < 2 * 148)
+    return NS == 128 ? launch_scan<128, 1>(a, s) : launch_scan<64, 1>(a, s);
+  return NS == 128 ? launch_scan<128, 4>(a, s) : launch_scan<64, 4>(a, s);
 }
 
-// CTAs that share a group's B and C in a decode step, if they can be one cluster (8 at most, the
-// portable size); 0: the conv is a kernel of its own.
-static int step_cluster(int H, int G, int P) {
-  const int n = (H / G) * (P / gdn::kScanRows);
-  return n <= 8 ? n : 0;
-}
-
-template <typename T, typename TS, int NS>
-static cudaError_t launch_step(const gdn::SsmArgs& a, const char* name, cudaStream_t s) {
-  const dim3 grid((unsigned)a.N * a.H * (a.P / gdn::kScanRows));
-  const int cluster = step_cluster(a.H, a.G, a.P);
-  if (cluster > 0)
-    return launch_ssm(false, cluster, gdn::ssm_step_kernel<T, TS, NS, true>, grid, 0, s, a, name);
-  cudaError_t e = launch_ssm(false, 1, gdn::ssm_conv_step_kernel<T>,
-                             dim3((a.Cc / 8 + 127) / 128, a.N), 0, s, a, "ssm_conv_step");
-  if (e != cudaSuccess) return e;
-  return launch_ssm(true, 1, gdn::ssm_step_kernel<T, TS, NS, false>, grid, 0, s, a, name);
+// Blocks of 64 state rows that share a group's B and C, and what a CTA may have of them (its conv
+// outputs are in shared memory).
+static int step_blocks(int H, int G, int P) { return (H / G) * (P / gdn::kScanRows); }
+constexpr int kStepCluster = 8, kStepMost = 128;
+// CTAs per group: enough to give each of 148 SMs its four CTAs twice over.  Once over, 83 sequences of
+// 32 heads of 128 x 128 take 72 us and not 62; four times over, 128 of them 93 us and not 89 (more
+// CTAs repeat the conv of B and C more often, fewer leave SMs without work at the end).
+constexpr int kStepCtas = 148 * 4 * 2;
+static int step_cluster(int N, int G, int R) {
+  int cl = 1;
+  while (cl < kStepCluster && cl < R &&
+         ((int64_t)N * G * cl < kStepCtas || (R + cl - 1) / cl > kStepMost))
+    cl *= 2;
+  return std::min(cl, R);
 }
 
 template <typename T, typename TS>
-static cudaError_t launch_step_n(const gdn::SsmArgs& a, int NS, const char* name, cudaStream_t s) {
-  return NS == 128 ? launch_step<T, TS, 128>(a, name, s) : launch_step<T, TS, 64>(a, name, s);
+static cudaError_t launch_step(const gdn::SsmArgs& a, int NS, const char* name, cudaStream_t s) {
+  const int R = step_blocks(a.H, a.G, a.P);
+  const int cl = step_cluster(a.N, a.G, R), nb = (R + cl - 1) / cl;
+  const dim3 grid((unsigned)a.N * a.G * cl);
+  const size_t smem = (2 * NS + (gdn::kScanRows + 2) * nb) * sizeof(float);
+  return NS == 128 ? launch_ssm(name, false, cl, gdn::ssm_step_kernel<T, TS, 128>, grid, smem, s, a,
+                                cl, nb)
+                   : launch_ssm(name, false, cl, gdn::ssm_step_kernel<T, TS, 64>, grid, smem, s, a,
+                                cl, nb);
 }
 
 static cudaError_t launch_ssm_decode(bool bf16, bool state_bf16, const gdn::SsmArgs& a, int NS,
                                      cudaStream_t s) {
   const char* name = state_bf16 ? "ssm_decode_step_bf16_state" : "ssm_decode_step";
   if (bf16)
-    return state_bf16 ? launch_step_n<__nv_bfloat16, __nv_bfloat16>(a, NS, name, s)
-                      : launch_step_n<__nv_bfloat16, float>(a, NS, name, s);
-  return state_bf16 ? launch_step_n<float, __nv_bfloat16>(a, NS, name, s)
-                    : launch_step_n<float, float>(a, NS, name, s);
+    return state_bf16 ? launch_step<__nv_bfloat16, __nv_bfloat16>(a, NS, name, s)
+                      : launch_step<__nv_bfloat16, float>(a, NS, name, s);
+  return state_bf16 ? launch_step<float, __nv_bfloat16>(a, NS, name, s)
+                    : launch_step<float, float>(a, NS, name, s);
 }
 
 }  // namespace gdn_host
@@ -568,18 +631,11 @@ int gdn_ssm_prefill_slots(const gdn_ssm_dims* dims, gdn_dtype dtype, const void*
                           conv_pool, out, workspace, workspace_bytes, dev_status, stream);
 }
 
-size_t gdn_ssm_decode_workspace_size(const gdn_ssm_dims* dims, int32_t batch) {
-  if (check_ssm_dims(dims) != GDN_OK || batch < 0) return 0;
-  if (gdn_host::step_cluster(dims->num_heads, dims->num_groups, dims->head_dim) > 0) return 0;
-  return (size_t)batch * ssm_channels(dims) * 4;
-}
-
 int gdn_ssm_decode_step(const gdn_ssm_dims* dims, gdn_dtype dtype, gdn_dtype state_dtype,
                         const void* x, const void* conv_w, const void* conv_b, const float* dt,
                         const float* dt_bias, const float* a_log, const float* D, const void* z,
                         void* conv_state, void* S, const int32_t* slot_idx, int32_t num_slots,
-                        int32_t batch, void* out, void* workspace, size_t workspace_bytes,
-                        int32_t* dev_status, void* stream) {
+                        int32_t batch, void* out, int32_t* dev_status, void* stream) {
   int rc = check_ssm_dims(dims);
   if (rc) return rc;
   if (!ssm_dtype_ok(dtype) || !ssm_dtype_ok(state_dtype)) return GDN_ERR_UNSUPPORTED;
@@ -590,14 +646,12 @@ int gdn_ssm_decode_step(const gdn_ssm_dims* dims, gdn_dtype dtype, gdn_dtype sta
   const void* ptrs[] = {x, conv_w, conv_b, dt, dt_bias, a_log, D, z, conv_state, S, out};
   for (const void* p : ptrs)
     if (p && misaligned(p)) return GDN_ERR_INVALID_ARG;
-  if (workspace && misaligned(workspace, 256)) return GDN_ERR_INVALID_ARG;
-  // grids: (sequence, head, 64 rows), and the sequences as the second dimension of the conv's
-  if (batch > 65535 ||
-      (int64_t)batch * dims->num_heads * (dims->head_dim / gdn::kScanRows) > INT32_MAX)
+  // the grid covers every (sequence, group, CTA of its cluster); a CTA holds its conv outputs
+  if ((int64_t)batch * dims->num_groups * gdn_host::kStepCluster > INT32_MAX ||
+      gdn_host::step_blocks(dims->num_heads, dims->num_groups, dims->head_dim) >
+          gdn_host::kStepCluster * gdn_host::kStepMost)
     return GDN_ERR_UNSUPPORTED;
   if (batch == 0) return GDN_OK;
-  const size_t need = gdn_ssm_decode_workspace_size(dims, batch);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
   gdn::SsmArgs a = ssm_args(dims);
   a.x = x;
   a.conv_w = conv_w;
@@ -607,13 +661,11 @@ int gdn_ssm_decode_step(const gdn_ssm_dims* dims, gdn_dtype dtype, gdn_dtype sta
   a.a_log = a_log;
   a.D = D;
   a.z = z;
-  a.S0 = S;
   a.SN = S;
   a.convN = conv_state;
   a.out = out;
   a.slot = slot_idx;
   a.status = dev_status;
-  a.u = static_cast<float*>(workspace);
   a.num_slots = num_slots;
   a.N = a.T = batch;
   return gdn_host::launch_ssm_decode(dtype == GDN_BF16, state_dtype == GDN_BF16, a,

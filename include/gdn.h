@@ -403,17 +403,13 @@ int gdn_ssm_prefill_slots(const gdn_ssm_dims* dims, gdn_dtype dtype, const void*
  *   conv_state [slots, K-1, Cc] and S [slots, H, P, N] in/out; state_dtype: type of S (GDN_F32, or
  *   GDN_BF16: read, updated in fp32 and rounded to nearest even once when written back);
  *   slot_idx [B] int32 nullable, num_slots, skipped slots, dev_status: as gdn_decode_step.
- *   workspace: at least gdn_ssm_decode_workspace_size() bytes, 256-byte aligned (the conv outputs
- *   of the step, fp32); calls that may overlap on the GPU need one each.  Layers with up to 512
- *   channels of x per group need none (size 0, NULL).
+ * One launch, no workspace.  GDN_ERR_UNSUPPORTED above 65,536 channels of x per group.
  */
-size_t gdn_ssm_decode_workspace_size(const gdn_ssm_dims* dims, int32_t batch);
 int gdn_ssm_decode_step(const gdn_ssm_dims* dims, gdn_dtype dtype, gdn_dtype state_dtype,
                         const void* x, const void* conv_w, const void* conv_b, const float* dt,
                         const float* dt_bias, const float* a_log, const float* D, const void* z,
                         void* conv_state, void* S, const int32_t* slot_idx, int32_t num_slots,
-                        int32_t batch, void* out, void* workspace, size_t workspace_bytes,
-                        int32_t* dev_status, void* stream);
+                        int32_t batch, void* out, int32_t* dev_status, void* stream);
 
 /*
  * gdn_batch_tables -- the index tables of one serving step, from the requests' lengths, in one

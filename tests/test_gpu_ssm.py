@@ -37,6 +37,15 @@ def test_prefill(shape, lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N", [64, 128])
+def test_prefill_many_heads_and_sequences(N, dtype):
+    # enough (sequence, head) pairs for a CTA to take 64 rows of a state in fp32
+    shape, lens = (32, 4, 64, N), (3, 20, 1, 0, 17, 33, 2, 1, 40, 5)
+    i = U.inputs(*shape, lens, dtype, seed=6)
+    U.check_layer(prefill(i, gdn.SsmDims(*shape)), U.layer(i, *shape), dtype, f"many {N}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("off", ["init", "gate", "bias", "direct"])
 def test_prefill_without_an_optional_part(off, dtype):
     shape, lens = (4, 2, 64, 128), (130, 3)

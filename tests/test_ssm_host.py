@@ -32,11 +32,6 @@ def test_shapes(L):
     assert f(ref(), 1, 0, 0) > 0 and f(ref(), 0, 0, 0) > 0
     assert f(None, 1, 1, 100) == 0 and f(ref(), 1, -1, 5) == 0 and f(ref(), 4, 1, 5) == 0
     assert f(ref(head_dim=96), 1, 1, 100) == 0
-    assert L.gdn_ssm_decode_workspace_size(ref(), -1) == 0
-    # up to 8 CTAs of 64 state rows per group are one cluster and need none
-    assert L.gdn_ssm_decode_workspace_size(ref(), 3) == 0
-    assert L.gdn_ssm_decode_workspace_size(ref(num_groups=4), 3) >= \
-        3 * gdn.SsmDims(num_groups=4).channels * 4
 
 
 def prefill(L, dims, dtype=1, x=A, w=A, b=None, dt=A, a_log=A, z=None, cu=A, N=1, T=16, S0=None,
@@ -79,20 +74,18 @@ def test_slots_refusals(L):
 
 
 def test_decode_refusals(L):
-    def call(dims=ref(num_groups=1), dtype=1, state=0, x=A, w=A, dt=A, a_log=A, conv=A, S=A, slot=A, slots=4,
-             B=2, out=A, ws=A, ws_bytes=1 << 40):
+    def call(dims=ref(), dtype=1, state=0, x=A, w=A, dt=A, a_log=A, conv=A, S=A, slot=A, slots=4,
+             B=2, out=A):
         return L.gdn_ssm_decode_step(dims, dtype, state, x, w, None, dt, None, a_log, None, None,
-                                     conv, S, slot, slots, B, out, ws, ws_bytes, None, None)
+                                     conv, S, slot, slots, B, out, None, None)
     for kw, want in ((dict(dims=None), BAD), (dict(dtype=3), UNSUP), (dict(state=3), UNSUP),
                      (dict(x=None), BAD), (dict(w=None), BAD), (dict(dt=None), BAD),
                      (dict(a_log=None), BAD), (dict(conv=None), BAD), (dict(S=None), BAD),
                      (dict(out=None), BAD), (dict(S=MIS), BAD), (dict(conv=MIS), BAD),
                      (dict(B=-1), BAD), (dict(slots=-1), BAD), (dict(slot=None, slots=1), BAD),
-                     (dict(ws=None), WS), (dict(ws_bytes=100), WS),
-                     (dict(ws=P((1 << 20) + 16)), BAD), (dict(B=70000), UNSUP)):
+                     (dict(B=1 << 30), UNSUP), (dict(dims=ref(num_heads=2048, num_groups=1)), UNSUP)):
         assert call(**kw) == want, kw
-    assert call(B=0, x=None, w=None, dt=None, a_log=None, conv=None, S=None, out=None,
-                ws=None) == gdn.GDN_OK
+    assert call(B=0, x=None, w=None, dt=None, a_log=None, conv=None, S=None, out=None) == gdn.GDN_OK
 
 
 def test_tables_refusals(L):
