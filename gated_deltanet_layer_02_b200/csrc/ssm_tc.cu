@@ -274,6 +274,53 @@ __device__ __forceinline__ Unit find_unit(const SsmArgs& a, int tokens, bool emp
   return r;
 }
 
+// find_unit for up to 32 sequences (one per lane) with the units in descending order of length: the
+// whole segments (`seg` chunks) first, then the sequences' last units by length.  Long work begins
+// first then, and 8 sequences of 20 to 56 chunks leave no SM alone at the end.
+__device__ __forceinline__ Unit find_unit_by_length(const SsmArgs& a, int seg, int k,
+                                                    int most_units) {
+  const int lane = threadIdx.x & 31;
+  int s = 0, e = 0;
+  if (lane < a.N) seq_range(a, lane, s, e);
+  const uint32_t nc = (uint32_t)(e - s + kL - 1) / kL, whole = nc / (uint32_t)seg;
+  const uint32_t rest = nc - whole * seg;
+  const bool last = lane < a.N && (rest > 0 || nc == 0);
+  const uint32_t nu = whole + (last ? 1 : 0);
+  // sums over the sequences before: chunks (64 bits: sequences may overlap), units, whole segments
+  uint64_t cs = nc;
+  uint32_t us = nu, ws = whole;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t c = __shfl_up_sync(0xffffffffu, cs, o);
+    const uint32_t u = __shfl_up_sync(0xffffffffu, us, o), w = __shfl_up_sync(0xffffffffu, ws, o);
+    if (lane >= o) {
+      cs += c;
+      us += u;
+      ws += w;
+    }
+  }
+  const uint32_t all = __shfl_sync(0xffffffffu, ws, 31);
+  uint32_t rank = all;  // place of the sequence's last unit
+  for (int m = 0; m < a.N; ++m) {
+    const uint32_t r = __shfl_sync(0xffffffffu, rest, m);
+    const bool l = __shfl_sync(0xffffffffu, (int)last, m);
+    if (l && (r > rest || (r == rest && m < lane))) ++rank;
+  }
+  const uint32_t w0 = ws - whole, kk = (uint32_t)k;
+  const bool in_whole = kk >= w0 && kk < ws, mine = in_whole || (last && kk == rank);
+  Unit r{lane, (int)(in_whole ? kk - w0 : whole), s, e, (int)(cs - nc), (int)(us - nu)};
+  if (mine && (cs > (uint64_t)(a.T / kL + a.N) || us > (uint32_t)most_units)) {
+    report_status(a.status, GDN_ERR_INVALID_ARG);  // sequences that overlap: see find_unit
+    r.e = r.s;
+    if (r.j > 0) r.n = -1;
+  }
+  const uint32_t who = __ballot_sync(0xffffffffu, mine);
+  if (!who) return Unit{-1, 0, 0, 0, 0, 0};
+  const bool it = lane == __ffs(who) - 1;
+  return Unit{uniform(it ? r.n : -1), uniform(it ? r.j : 0),     uniform(it ? r.s : 0),
+              uniform(it ? r.e : 0),  uniform(it ? r.chunk : 0), uniform(it ? r.first : 0)};
+}
+
 // ------------------------------------------------------------------------------------- bc
 // 512 threads: warp w has tokens 8 w .. 8 w + 7 of the chunk, first of B, then of C; a lane holds 4
 // channels of a row.  State widths below 128 are padded with zero channels.
@@ -859,8 +906,9 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
   pdl_trigger();
   const int slices = (a.H / a.G) * (a.P / 64), pairs = (slices + 1) / 2;
   const int grp = (blockIdx.x % (a.G * pairs)) / pairs, pair = blockIdx.x % pairs;
-  const Unit un = find_unit(a, g.seg * kL, true, blockIdx.x / (a.G * pairs),
-                            gridDim.x / (a.G * pairs));
+  const int unit = blockIdx.x / (a.G * pairs), units = gridDim.x / (a.G * pairs);
+  const Unit un = a.N <= 32 ? find_unit_by_length(a, g.seg, unit, units)
+                            : find_unit(a, g.seg * kL, true, unit, units);
   if (un.n < 0) {
     pdl_wait();
     return;
@@ -1255,13 +1303,17 @@ namespace {
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Chunks per segment.  A CTA works on 128 channels of one segment, so a call has pairs x units
-// CTAs, one per SM; the units are chosen so that they fill whole waves of the GPU, with the least
-// total of chunks one after the other.
+// CTAs, one per SM.  One sequence: as many units as fill whole waves of the GPU, with the least
+// total of chunks one after the other.  Several (whose lengths only the device knows): an SM's even
+// share of the chunks, so that a sequence is cut only if it alone would keep its SMs longer than
+// the whole call should take; every other cut costs a second conv and state update.  8 sequences of
+// 20 to 56 chunks (bf16, 80 heads of 64): a call took 1209 us with up to 4 waves and the units in
+// order, and takes 966 us so.
 int ssm_segment(int N, int T, int pairs) {
   constexpr int kSms = 148;
   const int chunks = std::max(1, T / gdn::kL + N);
   int best = chunks, cost = INT32_MAX;
-  for (int waves = 1; waves <= 4; ++waves) {
+  for (int waves = 1; waves <= (N > 1 ? 1 : 4); ++waves) {
     const int units = kSms * waves / pairs;
     if (units < 1) continue;
     const int seg = (chunks + units - 1) / units;
