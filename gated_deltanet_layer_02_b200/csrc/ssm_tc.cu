@@ -1307,7 +1307,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // total of chunks one after the other.  Several (whose lengths only the device knows): an SM's even
 // share of the chunks, so that a sequence is cut only if it alone would keep its SMs longer than
 // the whole call should take; every other cut costs a second conv and state update.  8 sequences of
-// 20 to 56 chunks (bf16, 80 heads of 64): a call took 1209 us with up to 4 waves and the units in
+// 20 to 56 chunks (bf16, 64 heads of 64): a call took 1209 us with up to 4 waves and the units in
 // order, and takes 966 us so.
 int ssm_segment(int N, int T, int pairs) {
   constexpr int kSms = 148;
