@@ -205,16 +205,20 @@ constexpr int kTargetS = 14;
 constexpr int kTargetW = 12;   // wX below 2^14 (two factors, each below 2 of its exponent)
 
 // Unit k of the packed batch: sequences cut into units of `tokens`, numbered sequence by
-// sequence; with `empty` a sequence without tokens has one unit too.  Every warp finds it by
-// itself, 128 sequences at a time (4 per lane).  `most_units`: units the launch has room for.
+// sequence.  A sequence without tokens has no chunk (kChunks) but one segment (kSegments: its state
+// is written too); kFollowed numbers the segments that another one follows, one fewer than a
+// sequence's segments, so that a batch of short sequences starts no CTA for them (96 sequences, 24
+// heads of 64: a call 169 -> 148 us).  Every warp finds its unit by itself, 128
+// sequences at a time (4 per lane).  `most_units`: units the launch has room for.
+enum UnitKind { kChunks, kSegments, kFollowed };
 struct Unit {
   int n;        // sequence, or -1: no such unit
   int j;        // unit inside the sequence
   int s, e;     // its sequence's tokens
   int chunk;    // first chunk of the sequence
-  int first;    // first unit of the sequence
+  int first;    // first segment of the sequence (kChunks: first chunk)
 };
-__device__ __forceinline__ Unit find_unit(const SsmArgs& a, int tokens, bool empty, int k,
+__device__ __forceinline__ Unit find_unit(const SsmArgs& a, int tokens, UnitKind kind, int k,
                                           int most_units) {
   const int lane = threadIdx.x & 31;
   const int64_t most = (int64_t)a.T / kL + a.N;  // chunks the workspace holds
@@ -229,8 +233,11 @@ __device__ __forceinline__ Unit find_unit(const SsmArgs& a, int tokens, bool emp
       s[q] = e[q] = 0;
       if (n < a.N) seq_range(a, n, s[q], e[q]);
       nc[q] = (uint32_t)(e[q] - s[q] + kL - 1) / kL;
-      nu[q] = n < a.N ? max((uint32_t)(e[q] - s[q] + tokens - 1) / (uint32_t)tokens, empty ? 1u : 0u)
-                      : 0u;
+      const uint32_t followed = ((uint32_t)max(e[q] - s[q], 1) - 1) / (uint32_t)tokens;
+      nu[q] = n >= a.N             ? 0u
+              : kind == kSegments  ? followed + 1
+              : kind == kFollowed  ? followed
+                                   : (uint32_t)(e[q] - s[q] + tokens - 1) / (uint32_t)tokens;
       us += nu[q];
       cs += nc[q];
     }
@@ -250,12 +257,13 @@ __device__ __forceinline__ Unit find_unit(const SsmArgs& a, int tokens, bool emp
     for (int q = 0; q < 4; ++q) {
       if (k >= uf && k < uf + nu[q]) {
         mine = true;
-        r = Unit{base + 4 * lane + q, (int)(k - uf), s[q], e[q], (int)cf, (int)uf};
+        const int n = base + 4 * lane + q;
+        r = Unit{n, (int)(k - uf), s[q], e[q], (int)cf, (int)uf + (kind == kFollowed ? n : 0)};
         if (cf + nc[q] > most || uf + nu[q] > most_units) {
           // sequences that overlap: no room for this one, it counts as empty
           report_status(a.status, GDN_ERR_INVALID_ARG);
           r.e = r.s;
-          if (r.j > 0 || !empty) r.n = -1;
+          if (r.j > 0 || kind != kSegments) r.n = -1;
         }
       }
       uf += nu[q];
@@ -404,7 +412,7 @@ __global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ 
   pdl_trigger();
   const int roles = a.G + (a.H + kGateHeads - 1) / kGateHeads;
   const int grp = blockIdx.x % roles;
-  const Unit un = find_unit(a, kL, false, blockIdx.x / roles, gridDim.x / roles);
+  const Unit un = find_unit(a, kL, kChunks, blockIdx.x / roles, gridDim.x / roles);
   if (un.n < 0) return;
   if (grp >= a.G) {
     gates(g, un, grp - a.G, reinterpret_cast<float*>(sm));
@@ -719,13 +727,11 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(const __grid_constant__
   pdl_trigger();
   const int slices = (a.H / a.G) * (a.P / 64), pairs = (slices + 1) / 2;
   const int grp = (blockIdx.x % (a.G * pairs)) / pairs, pair = blockIdx.x % pairs;
-  const Unit un = find_unit(a, g.seg * kL, true, blockIdx.x / (a.G * pairs),
+  const Unit un = find_unit(a, g.seg * kL, kFollowed, blockIdx.x / (a.G * pairs),
                             gridDim.x / (a.G * pairs));
   pdl_wait();  // before any return: the next kernel counts on this one having waited
   if (un.n < 0) return;
-  const int total = (un.e - un.s + kL - 1) / kL;  // chunks of the sequence
-  const int c0 = un.j * g.seg, c1 = c0 + g.seg;
-  if (c1 >= total) return;  // no segment follows
+  const int c0 = un.j * g.seg, c1 = c0 + g.seg;  // whole: another segment follows
 
   const int wid = uniform(tid >> 5), pipe = wid >> 3, pw = wid & 7, pt = tid & 255;
   uint8_t* ctl = sm + kSegCtl;
@@ -861,7 +867,8 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(const __grid_constant__
           const float* S0 = a.S0 && row >= 0
                                 ? static_cast<const float*>(a.S0) + (size_t)row * pitch + base
                                 : nullptr;
-          float* keep = g.seg_state + (size_t)(un.first + (total - 1) / g.seg) * pitch + base;
+          const int last = ((un.e - un.s + kL - 1) / kL - 1) / g.seg;  // segment of the sequence
+          float* keep = g.seg_state + (size_t)(un.first + last) * pitch + base;
           const float dec = exp2f((float)R);
 #pragma unroll
           for (int q = 0; q < 32; ++q) {
@@ -908,7 +915,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
   const int grp = (blockIdx.x % (a.G * pairs)) / pairs, pair = blockIdx.x % pairs;
   const int unit = blockIdx.x / (a.G * pairs), units = gridDim.x / (a.G * pairs);
   const Unit un = a.N <= 32 ? find_unit_by_length(a, g.seg, unit, units)
-                            : find_unit(a, g.seg * kL, true, unit, units);
+                            : find_unit(a, g.seg * kL, kSegments, unit, units);
   if (un.n < 0) {
     pdl_wait();
     return;
@@ -1399,8 +1406,8 @@ cudaError_t launch_ssm_tc(gdn::SsmTcArgs g, void* workspace, cudaStream_t s) {
   cudaError_t e = launch_tc(false, gdn::ssm_bc_kernel, (unsigned)(a.T / gdn::kL + a.N) * roles, 512,
                             gdn::kBcSmem, s, g, "ssm_bc");
   if (e == cudaSuccess && a.T > l.seg * gdn::kL)  // a sequence may have several segments
-    e = launch_tc(true, gdn::ssm_seg_kernel, (unsigned)l.units * pairs, 512, gdn::kSegSmem, s, g,
-                  "ssm_seg");
+    e = launch_tc(true, gdn::ssm_seg_kernel, (unsigned)(a.T / (l.seg * gdn::kL)) * pairs, 512,
+                  gdn::kSegSmem, s, g, "ssm_seg");
   if (e == cudaSuccess)
     e = launch_tc(true, gdn::ssm_main_kernel, (unsigned)l.units * pairs, 512, gdn::kMainSmem, s, g,
                   "ssm_main");
