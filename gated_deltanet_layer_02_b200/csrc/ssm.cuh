@@ -18,10 +18,10 @@ __device__ __forceinline__ void seq_range(const SsmArgs& a, int n, int& s, int& 
   }
 }
 
-// softplus(v) = max(v, 0) + log1p(exp(-|v|)), within [lo, hi]
+// softplus(v) = max(v, 0) + log1p(exp(-|v|)), within [lo, hi]; a NaN stays one
 __device__ __forceinline__ float ssm_step(float v, float lo, float hi) {
   const float sp = fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
-  return fminf(fmaxf(sp, lo), hi);
+  return sp < lo ? lo : (sp > hi ? hi : sp);
 }
 
 template <typename T>

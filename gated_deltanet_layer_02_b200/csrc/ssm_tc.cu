@@ -368,8 +368,9 @@ __device__ __forceinline__ void gates(const SsmTcArgs& g, const Unit& un, int pa
     double c[4], sum = 0.0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      // a decay below 2^-150 counts as 2^-150 (zero in fp32)
-      sum += (double)fmaxf(rate2 * d[e], -150.f);
+      // a decay below 2^-150 counts as 2^-150 (zero in fp32); a NaN stays one
+      const float l = rate2 * d[e];
+      sum += (double)(l < -150.f ? -150.f : l);
       c[e] = sum;
     }
     double inc = sum;
@@ -378,7 +379,8 @@ __device__ __forceinline__ void gates(const SsmTcArgs& g, const Unit& un, int pa
       const double up = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += up;
     }
-    const double all = __shfl_sync(0xffffffffu, inc, 31), before = inc - sum;
+    const double all = __shfl_sync(0xffffffffu, inc, 31);
+    const double up = __shfl_up_sync(0xffffffffu, inc, 1), before = lane ? up : 0.0;
     const double start = __shfl_sync(0xffffffffu, before, lane & 24);  // of the block of 32 tokens
     const double stop = __shfl_sync(0xffffffffu, inc, lane | 7);
     float4 w, lf, cum;
@@ -389,7 +391,8 @@ __device__ __forceinline__ void gates(const SsmTcArgs& g, const Unit& un, int pa
     for (int e = 0; e < 4; ++e) {
       const double ce = before + c[e];
       pw[e] = d[e] * exp2f((float)(all - ce));
-      pl[e] = (float)((double)fmaxf(log2f(d[e]), -1000.f) - (ce - start));
+      const float l = log2f(d[e]);
+      pl[e] = (float)((double)(l < -1000.f ? -1000.f : l) - (ce - start));
       pc[e] = (float)(ce - start);
     }
     const size_t at = (size_t)(un.chunk + un.j) * a.H + h;

@@ -301,3 +301,47 @@ def test_two_calls_at_once():
     for k in range(2):
         for r in got[k]:
             assert all(torch.equal(a, b) for a, b in zip(r, alone[k]))
+
+
+def _isolated(clean, broken, cu, seq, t, head, width):
+    """`broken` has a non-finite input at token t of sequence `seq` and head `head`: the head's
+    outputs from there on (`width` channels of them) and its state are not finite, and everything
+    else has the bits of `clean`."""
+    at, end = int(cu[seq]) + t, int(cu[seq + 1])
+    ch = slice(0, width)
+    assert not torch.any(torch.isfinite(broken[0][at:end, head, ch].float()))
+    assert not torch.any(torch.isfinite(broken[1][seq, head, ch]))
+    keep = torch.ones_like(clean[0], dtype=torch.bool)
+    keep[at:end, head, ch] = False
+    assert torch.equal(broken[0][keep], clean[0][keep])
+    keep = torch.ones_like(clean[1], dtype=torch.bool)
+    keep[seq, head, ch] = False
+    assert torch.equal(broken[1][keep], clean[1][keep])
+
+
+@pytest.mark.parametrize("t", [0, 37, 130, 299])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_nan_step_reaches_its_head_from_its_token_on(dtype, t):
+    shape, lens = (4, 2, 128, 128), (50, 300, 60)
+    dims = gdn.SsmDims(*shape)
+    i = U.inputs(*shape, lens, dtype, seed=31)
+    clean = prefill(i, dims)
+    i["dt"][50 + t, 2] = float("nan")
+    _isolated(clean, prefill(i, dims), i["cu"], 1, t, 2, 128)
+
+
+def test_nan_step_of_one_token():
+    shape, B = (4, 2, 64, 128), 3
+    dims = gdn.SsmDims(*shape)
+    i = U.inputs(*shape, (1,) * B, BF, seed=32)
+    ensure_built()
+
+    def step():
+        S, c = dev(i["S0"]), dev(i["conv0"])
+        o = gdn.ssm_decode_step(dev(i["x"]), dev(i["dt"]), dev(i["a_log"]), c, S, dev(i["conv_w"]),
+                                dims=dims)
+        return o, S
+
+    clean = step()
+    i["dt"][1, 3] = float("nan")
+    _isolated(clean, step(), i["cu"], 1, 0, 3, 64)
