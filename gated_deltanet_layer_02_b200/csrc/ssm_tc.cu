@@ -13,7 +13,10 @@
 // rows of X and B: g_j = log2(delta_j) - cum_j + eX_j + eB_j, pm_i = max over j <= i of g_j,
 //   P^_ij = (C^_i.B^_j) 2^(g_j - pm_i)
 // (never above the product), and row i of the result counts 2^(cum_i + pm_i + exponent of C_i).
-// A NaN or infinity in x reaches outputs of its whole chunk (zero weights do not remove it).
+// Non-finite values.  Zero weights would not remove them, and as a row's largest value they would
+// scale its other values away.  So a row of X that holds one counts as zero in X^, and the token's
+// weights in P and wX as NaN: the 64 channels of such a token are NaN from it on, what came before
+// stays.  A row of B that holds one is NaN throughout; C only concerns its own token.
 //
 // Kernels (programmatic dependent launch between them):
 //   bc    per (chunk, group): conv of B and C; the operand tiles C^ and B (two parts) in the
@@ -185,8 +188,14 @@ __device__ __forceinline__ float2 silu2(float2 x) {
   return __fmul2_rn(x, mul2(make_float2(d.y, d.x), rcp(d.x * d.y)));
 }
 
-// Exponent of the largest magnitude of a row (its bits), within [-100, 127]; the row is scaled
-// by pow2(target - exponent).
+// Exponent of the largest magnitude of a row (its bits), within [-100, 127], or 128 for a row that
+// holds an infinity or NaN (kept as the int8 -128); the row is scaled by pow2(target - exponent).
+constexpr int kNotFinite = 128;
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 __device__ __forceinline__ int exponent_of(uint32_t bits) {
   return max((int)(bits >> 23) - 127, -100);
@@ -489,8 +498,8 @@ __global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ 
         if (i0 + q >= L) u[p] = make_float2(0.f, 0.f);
       }
       const uint32_t top = __reduce_max_sync(
-          0xffffffffu, __float_as_uint(fmaxf(fmaxf(fabsf(u[0].x), fabsf(u[0].y)),
-                                             fmaxf(fabsf(u[1].x), fabsf(u[1].y)))));
+          0xffffffffu, __float_as_uint(max_nan(max_nan(fabsf(u[0].x), fabsf(u[0].y)),
+                                               max_nan(fabsf(u[1].x), fabsf(u[1].y)))));
       if (lane == q) tops = top;
       const float sc = pow2((part ? kTargetC : kTargetB) - exponent_of(top));
       uint2 hi, lo;
@@ -504,6 +513,15 @@ __global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ 
       if (!part) *reinterpret_cast<uint2*>(hi_out + 2 * kTileB + off) = lo;
     }
     if (lane < 8) ex[part * kL + i0 + lane] = (int8_t)exponent_of(tops);
+    uint32_t lost = __ballot_sync(0xffffffffu, lane < 8 && exponent_of(tops) == kNotFinite);
+    for (; lost; lost &= lost - 1) {  // such a row: NaN throughout (the lane rewrites its own)
+      const int q = __ffs(lost) - 1;
+      const uint32_t off = ((lane >> 4) * kTileB + (i0 + q) * 128 +
+                            (((((lane & 15) >> 1) ^ q) << 4) | (lane & 1) * 8));
+      const uint2 nan2 = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+      *reinterpret_cast<uint2*>(sm + part * 2 * kTileB + off) = nan2;
+      *reinterpret_cast<uint2*>(hi_out + off) = nan2;
+    }
   }
   fence_proxy_async_smem();
   __syncthreads();
@@ -644,7 +662,7 @@ __device__ __forceinline__ int conv_x(const Taps& tp, int L, int warp, int lane,
     if (q >= live) u = make_float2(0.f, 0.f);
     put(q, u);
     const uint32_t m =
-        __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(u.x), fabsf(u.y))));
+        __reduce_max_sync(0xffffffffu, __float_as_uint(max_nan(fabsf(u.x), fabsf(u.y))));
     if (lane == q) top = m;
   }
   const int e = exponent_of(top);
@@ -706,6 +724,10 @@ __device__ __forceinline__ int chunk_exponent(const float4& w4, uint32_t ex4, ui
 // pieces of row r are swizzled by r % 8.
 __device__ __forceinline__ uint32_t pair_off(int warp, int lane, int q) {
   return ((warp * kTok * 128 + ((lane >> 2) << 4) + (lane & 3) * 4) ^ ((q & 7) << 4)) + q * 128;
+}
+// w 2^e, the weight of a token whose row of X has exponent eX
+__device__ __forceinline__ float token_weight(float w, int eX, int e) {
+  return eX == kNotFinite ? __int_as_float(0x7fffffff) : scale2(w, e);
 }
 // Two parts of u w into the tiles at W (high) and W + kTileB (low).
 __device__ __forceinline__ void store_parts(float2 u, float w, uint8_t* W, uint32_t at) {
@@ -824,12 +846,13 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(const __grid_constant__
       wait_x();
       float2 u[kTok];
       int8_t* ex_s = ex2_s + (k & 1) * kL;
-      conv_x(taps, kL, warp, lane, raw, halo, ex_s, [&](int q, float2 v) { u[q] = v; });
+      const int eq =
+          conv_x(taps, kL, warp, lane, raw, halo, ex_s, [&](int q, float2 v) { u[q] = v; });
       __syncwarp();  // the warp has read its rows
       if (k + 1 < nch) load_x(g, un, s, t0 - kL, warp, lane, raw, halo);
       if (bar_or_n(1 + pipe, kPipe, !ok)) break;
       const int top = chunk_exponent(w4, reinterpret_cast<const uint32_t*>(ex_s)[lane], eB4);
-      const float wq = scale2(w, eB + kTargetW - top);
+      const float wq = token_weight(w, eq, eB + kTargetW - top);
       if (k > 0) take(k - 1);
       scale = scale2(exp2f((float)R), top - kTargetW - kTargetB);
       R += all;
@@ -1048,7 +1071,8 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
       top = __reduce_max_sync(0xffffffffu, top_s[lane & 7]);
       const int eS = exponent_of(top);
       {
-        const float sc = pow2(kTargetS - eS);
+        // (an infinity in the state: as a row of X that holds one)
+        const float sc = eS == kNotFinite ? __int_as_float(0x7fffffff) : pow2(kTargetS - eS);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint4 f;
@@ -1066,7 +1090,8 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
         const int own = warp * kTok + (lane & (kTok - 1));
         const uint32_t e4 = __shfl_sync(0xffffffffu, eB4, own >> 2);
         const int eB = (int)(int8_t)(e4 >> (8 * (own & 3)));
-        const float wq = scale2(w, eB + kTargetW - wt), xs = pow2(kTargetX - eq);
+        const float wq = token_weight(w, eq, eB + kTargetW - wt);
+        const float xs = pow2(kTargetX - eq);
 #pragma unroll
         for (int q0 = 0; q0 < kTok; q0 += 8) {  // eight loads, then their stores
           float2 u[8];
@@ -1085,9 +1110,12 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
           }
         }
       }
+      uint32_t lost = __ballot_sync(0xffffffffu, lane < kTok && eq == kNotFinite);
+      for (; lost; lost &= lost - 1)  // zero rows of X^ (the lane rewrites its own)
+        *reinterpret_cast<uint32_t*>(X + pair_off(warp, lane, __ffs(lost) - 1)) = 0u;
       // ---- g of token i, in units of its block's start
       const int eX = ex_s[i];
-      const float gi = lfi + (float)(eX + eBi);
+      const float gi = eX == -kNotFinite ? __int_as_float(0x7fffffff) : lfi + (float)(eX + eBi);
       if (half == 0) {
         // its running maximum, and the maxima M of the blocks (lane l: tokens 4 l ..)
         const float4 lf4 = ldgf4(gate + kL + 4 * lane);

@@ -345,3 +345,48 @@ def test_nan_step_of_one_token():
     clean = step()
     i["dt"][1, 3] = float("nan")
     _isolated(clean, step(), i["cu"], 1, 0, 3, 64)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")], ids=str)
+@pytest.mark.parametrize("t", [1, 100, 128, 298])
+def test_non_finite_x_reaches_its_channels_from_its_token_on(t, value):
+    # one channel of x of head 2 (its second 64 of 128); the chunked form makes the 64 NaN
+    shape, lens = (4, 2, 128, 128), (50, 300, 60)
+    dims = gdn.SsmDims(*shape)
+    i = U.inputs(*shape, lens, BF, seed=33)
+    i["conv_w"][2 * 128 + 70] = 1.0  # every tap passes it on
+    clean = prefill(i, dims)
+    i["x"][50 + t, 2 * 128 + 70] = value
+    o, S, _ = prefill(i, dims)
+    at, end, ch = 50 + t, 350, slice(64, 128)
+    assert not torch.any(torch.isfinite(o[at:end, 2, ch].float()))
+    assert not torch.any(torch.isfinite(S[1, 2, ch]))
+    for got, was in ((o, clean[0]), (S, clean[1])):
+        keep = torch.ones_like(was, dtype=torch.bool)
+        if got is o:
+            keep[at:end, 2, ch] = False
+        else:
+            keep[1, 2, ch] = False
+        assert torch.equal(got[keep], was[keep])
+
+
+@pytest.mark.parametrize("what", ["B", "C"])
+def test_non_finite_b_or_c_reaches_its_group_from_its_token_on(what):
+    shape, lens, t = (4, 2, 64, 128), (50, 300, 60), 140
+    dims = gdn.SsmDims(*shape)
+    i = U.inputs(*shape, lens, BF, seed=34)
+    c = 4 * 64 + (0 if what == "B" else 2 * 128) + 128 + 5  # of group 1: heads 2 and 3
+    i["conv_w"][c] = 1.0
+    clean = prefill(i, dims)
+    i["x"][50 + t, c] = float("inf")
+    o, S, _ = prefill(i, dims)
+    end = 350 if what == "B" else 50 + t + 4  # C: as long as the conv sees it
+    assert not torch.any(torch.isfinite(o[50 + t:end, 2:].float()))
+    keep = torch.ones_like(o, dtype=torch.bool)
+    keep[50 + t:end, 2:] = False
+    assert torch.equal(o[keep], clean[0][keep])
+    keep = torch.ones_like(S, dtype=torch.bool)
+    if what == "B":
+        assert not torch.any(torch.isfinite(S[1, 2:]))
+        keep[1, 2:] = False
+    assert torch.equal(S[keep], clean[1][keep])
