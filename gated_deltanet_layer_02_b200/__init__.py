@@ -617,6 +617,15 @@ def ssm_prefill_workspace_size(num_seqs: int, num_tokens: int, dtype=torch.bfloa
         num_seqs, num_tokens))
 
 
+def _ssm_rows(x, dims):
+    """Address of x [rows, Cc], its type's code, its rows and its device."""
+    code, Cc = _act_dtype(x), dims.channels
+    if x.dim() != 2 or x.shape[1] != Cc:
+        raise ValueError(f"x holds {list(x.shape)}; the call needs [rows, {Cc}]")
+    dev = x.get_device()
+    return _arg(x, "x", x.dtype, 0, dev), code, x.shape[0], dev
+
+
 def _ssm_weights(dims, dt_x, dev, conv_w, conv_b, dt, dt_bias, a_log, D, T):
     Cc, H = dims.channels, dims.num_heads
     return (_arg(conv_w, "conv_w", dt_x, Cc * dims.conv_kernel, dev, True),
@@ -638,10 +647,9 @@ def ssm_prefill(x, dt, a_log, cu_seqlens, conv_w, conv_b=None, dt_bias=None, D=N
     sequence (cu_seqlens[N] < T) are left as they were."""
     lib()
     dims = dims or SsmDims()
-    code, dtx, T, N = _act_dtype(x), x.dtype, x.shape[0], cu_seqlens.numel() - 1
+    px, code, T, dev = _ssm_rows(x, dims)
+    dtx, N = x.dtype, cu_seqlens.numel() - 1
     H, P, Ns, Cc = dims.num_heads, dims.head_dim, dims.state_dim, dims.channels
-    dev = x.get_device()
-    px = _arg(x, "x", dtx, T * Cc, dev)
     w = _ssm_weights(dims, dtx, dev, conv_w, conv_b, dt, dt_bias, a_log, D, T)
     pz = _arg(z, "z", dtx, T * H * P, dev)
     pcu = _arg(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev)
@@ -674,10 +682,9 @@ def ssm_prefill_slots(x, dt, a_log, cu_seqlens, S_pool, conv_w, slot_idx=None, c
     ([slots, 3, Cc]).  Slots as in chunk_prefill_slots.  Returns out [T, H, P]."""
     lib()
     dims = dims or SsmDims()
-    code, dtx, T, N = _act_dtype(x), x.dtype, x.shape[0], cu_seqlens.numel() - 1
+    px, code, T, dev = _ssm_rows(x, dims)
+    dtx, N = x.dtype, cu_seqlens.numel() - 1
     H, P = dims.num_heads, dims.head_dim
-    dev = x.get_device()
-    px = _arg(x, "x", dtx, T * dims.channels, dev)
     w = _ssm_weights(dims, dtx, dev, conv_w, conv_b, dt, dt_bias, a_log, D, T)
     pz = _arg(z, "z", dtx, T * H * P, dev)
     pcu = _arg(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev)
@@ -716,10 +723,8 @@ def ssm_decode_step(x, dt, a_log, conv_state, S, conv_w, conv_b=None, dt_bias=No
     device and reported in dev_status (GDN_ERR_INVALID_ARG)."""
     lib()
     dims = dims or SsmDims()
-    code, dtx, B = _act_dtype(x), x.dtype, x.shape[0]
-    H, P, Cc = dims.num_heads, dims.head_dim, dims.channels
-    dev = x.get_device()
-    px = _arg(x, "x", dtx, B * Cc, dev)
+    px, code, B, dev = _ssm_rows(x, dims)
+    dtx, H, P = x.dtype, dims.num_heads, dims.head_dim
     w = _ssm_weights(dims, dtx, dev, conv_w, conv_b, dt, dt_bias, a_log, D, B)
     pz = _arg(z, "z", dtx, B * H * P, dev)
     rows = _ssm_pool_rows(S, conv_state, dims)

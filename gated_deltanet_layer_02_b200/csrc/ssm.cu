@@ -21,15 +21,14 @@ constexpr int kConvRun = 16;    // tokens per thread of the packed conv
 
 // Packed prompts: a thread owns 8 channels and a run of kConvRun tokens, the three rows before
 // the current one in registers.
-template <typename T>
 __global__ void __launch_bounds__(128) ssm_conv_kernel(SsmArgs a) {
   pdl_trigger();
   const int c = (blockIdx.y * 128 + threadIdx.x) * 8, t0 = blockIdx.x * kConvRun;
   if (c >= a.Cc) return;
   float w[4][8], b[8];
-  load_taps<T>(a, c, w, b);
-  const T* x = static_cast<const T*>(a.x) + c;
-  const T* c0 = static_cast<const T*>(a.conv0);
+  load_taps<float>(a, c, w, b);
+  const float* x = static_cast<const float*>(a.x) + c;
+  const float* c0 = static_cast<const float*>(a.conv0);
   float h[3][8];
   int n = seq_of_token(a.cu, a.N, t0) - 1, s = 0, end = 0;
   const int t1 = min(a.T, t0 + kConvRun);
@@ -453,7 +452,7 @@ static cudaError_t launch_ssm_prefill(bool bf16, const gdn::SsmArgs& a, int NS, 
   }
   if (a.T > 0) {
     const dim3 grid((a.T + gdn::kConvRun - 1) / gdn::kConvRun, (a.Cc / 8 + 127) / 128);
-    cudaError_t e = launch_ssm("ssm_conv", false, 1, gdn::ssm_conv_kernel<float>, grid, 0, s, a);
+    cudaError_t e = launch_ssm("ssm_conv", false, 1, gdn::ssm_conv_kernel, grid, 0, s, a);
     if (e != cudaSuccess) return e;
   }
   // Rows per CTA: 16 where that is needed to have work for all SMs (a token costs one quad per warp
@@ -556,8 +555,8 @@ int ssm_prefill_impl(const gdn_ssm_dims* dims, gdn_dtype dtype, const void* x, c
   for (const void* p : ptrs)
     if (p && misaligned(p)) return GDN_ERR_INVALID_ARG;
   if (workspace && misaligned(workspace, 256)) return GDN_ERR_INVALID_ARG;
-  // a grid covers every (sequence or chunk, head, 64 rows)
-  if (((int64_t)N + T / 128) * dims->num_heads * (dims->head_dim / gdn::kScanRows) > INT32_MAX)
+  // a grid covers every (sequence or chunk, head, 64 rows), or (chunk, group, gates of 32 heads)
+  if (((int64_t)N + T / 128) * dims->num_heads * 2 > INT32_MAX)
     return GDN_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < gdn_ssm_prefill_workspace_size(dims, dtype, N, T))
     return GDN_ERR_WORKSPACE;

@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
-    if (!ok) wait_long(bar, 0, g.wait_ns);  // the product still in flight
+    if (!ok) wait_long(bar, 0, kWaitLimitNs);  // the product still in flight
     tmem_dealloc(tmem, 128);
   }
 }
@@ -910,7 +910,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(const __grid_constant__
     }
     if (!ok && pt == 0) {
       report_status(a.status, GDN_ERR_TIMEOUT);
-      if (mmas > 0) wait_long(done + pipe, (mmas - 1) & 1, g.wait_ns);
+      if (mmas > 0) wait_long(done + pipe, (mmas - 1) & 1, kWaitLimitNs);
     }
     wait_x();
   }
@@ -918,7 +918,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(const __grid_constant__
   __syncthreads();
   if (tid == 0)  // copies in flight, after a wait that ran out
     for (int k = 0; k < 2; ++k)
-      if (loads[k] > 0) wait_long(full + k, (loads[k] - 1) & 1, g.wait_ns);
+      if (loads[k] > 0) wait_long(full + k, (loads[k] - 1) & 1, kWaitLimitNs);
   if (tid < 32) tmem_dealloc(tmem, 128);
 }
 
@@ -1314,7 +1314,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
     }
     if (!ok && pt == 0) {
       report_status(a.status, GDN_ERR_TIMEOUT);
-      if (mmas > 0) wait_long(done + pipe, (mmas - 1) & 1, g.wait_ns);
+      if (mmas > 0) wait_long(done + pipe, (mmas - 1) & 1, kWaitLimitNs);
     }
     wait_x();
   }
@@ -1323,8 +1323,8 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *loads > 0) {  // copies in flight, after a wait that ran out
-    wait_long(c_full, (*loads - 1) & 1, g.wait_ns);
-    wait_long(b_full, (*loads - 1) & 1, g.wait_ns);
+    wait_long(c_full, (*loads - 1) & 1, kWaitLimitNs);
+    wait_long(b_full, (*loads - 1) & 1, kWaitLimitNs);
   }
   if (tid < 32) tmem_dealloc(tmem, 512);
 }
@@ -1347,14 +1347,14 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // the whole call should take; every other cut costs a second conv and state update.  8 sequences of
 // 20 to 56 chunks (bf16, 64 heads of 64): a call took 1209 us with up to 4 waves and the units in
 // order, and takes 966 us so.
-int ssm_segment(int N, int T, int pairs) {
-  constexpr int kSms = 148;
-  const int chunks = std::max(1, T / gdn::kL + N);
-  int best = chunks, cost = INT32_MAX;
-  for (int waves = 1; waves <= (N > 1 ? 1 : 4); ++waves) {
+constexpr int kSms = 148, kMostWaves = 4;
+int64_t ssm_segment(int N, int T, int pairs) {
+  const int64_t chunks = std::max<int64_t>(1, (int64_t)T / gdn::kL + N);
+  int64_t best = chunks, cost = INT64_MAX;
+  for (int waves = 1; waves <= (N > 1 ? 1 : kMostWaves); ++waves) {
     const int units = kSms * waves / pairs;
     if (units < 1) continue;
-    const int seg = (chunks + units - 1) / units;
+    const int64_t seg = (chunks + units - 1) / units;
     if (seg * waves < cost) {
       cost = seg * waves;
       best = seg;
@@ -1364,7 +1364,7 @@ int ssm_segment(int N, int T, int pairs) {
 }
 
 struct TcLayout {
-  int seg, units;
+  int64_t seg, units;  // chunks per segment, segments
   size_t tiles, cb, ex, hist, gate, block, decay, seg_state, seg_decay, total;
 };
 
@@ -1374,6 +1374,9 @@ TcLayout tc_layout(int N, int T, int H, int G, int P, int NS, int Cc) {
   const size_t chunks = (size_t)T / gdn::kL + N, blocks = chunks * G;
   l.seg = ssm_segment(N, T, pairs);
   l.units = T / (l.seg * gdn::kL) + N;
+  // room for the states of as many segments as any rule of ssm_segment makes: the size grows with N
+  // and with T, so a workspace for a server's largest batch takes the others too
+  const size_t room = std::min(T / gdn::kL, kSms * kMostWaves / pairs) + (size_t)N;
   size_t o = 0;
   l.tiles = o; o = up256(o + blocks * gdn::kBcBytes);
   l.cb = o; o = up256(o + blocks * gdn::kL * gdn::kL * 2);
@@ -1382,8 +1385,8 @@ TcLayout tc_layout(int N, int T, int H, int G, int P, int NS, int Cc) {
   l.gate = o; o = up256(o + chunks * H * 3 * gdn::kL * 4);
   l.block = o; o = up256(o + chunks * H * 4 * 4);
   l.decay = o; o = up256(o + chunks * H * 8);
-  l.seg_state = o; o = up256(o + (size_t)l.units * H * P * NS * 4);
-  l.seg_decay = o; o = up256(o + (size_t)l.units * H * 8);
+  l.seg_state = o; o = up256(o + room * H * P * NS * 4);
+  l.seg_decay = o; o = up256(o + room * H * 8);
   l.total = o;
   return l;
 }
@@ -1429,7 +1432,7 @@ cudaError_t launch_ssm_tc(gdn::SsmTcArgs g, void* workspace, cudaStream_t s) {
   g.decay = reinterpret_cast<double*>(w + l.decay);
   g.seg_state = reinterpret_cast<float*>(w + l.seg_state);
   g.seg_decay = reinterpret_cast<double*>(w + l.seg_decay);
-  g.seg = l.seg;
+  g.seg = (int)l.seg;
   g.wait_ns = debug_opts().wait_limit_us ? (uint64_t)debug_opts().wait_limit_us * 1000ull
                                          : gdn::kWaitLimitNs;
   const unsigned pairs = a.G * (((a.H / a.G) * (a.P / 64) + 1) / 2);

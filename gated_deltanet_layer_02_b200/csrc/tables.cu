@@ -98,12 +98,14 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(TableArgs a) 
       a.cu[a.N] = take ? (int)tok : 0;
     }
     const int total = take ? (int)tok : 0;
-    for (int r = max(r0, total) + tid; r < r1; r += kTabThreads) {
+    for (uint32_t r = max(r0, total) + tid; r < (uint32_t)r1; r += kTabThreads) {
       if (a.pos) a.pos[r] = -1;
       if (a.map) a.map[r] = -1;
     }
     if (!take)
-      for (int n = blockIdx.x * kTabThreads + tid; n < a.N; n += gridDim.x * kTabThreads) a.cu[n] = 0;
+      for (uint32_t n = blockIdx.x * kTabThreads + tid; n < (uint32_t)a.N;
+           n += gridDim.x * kTabThreads)
+        a.cu[n] = 0;
     return take;
   };
   if (!one) {
@@ -190,7 +192,8 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(TableArgs a) 
               p_hi = (int)(page0 + p_all);
     // this CTA's rows that belong to the block
     const int b1 = min(r1, t_hi);
-    for (int row = max(r0, t_lo) + tid; row < b1; row += kTabThreads) {
+    for (uint32_t u = max(r0, t_lo) + tid; u < (uint32_t)b1; u += kTabThreads) {
+      const int row = (int)u;
       const int i = last_at_most(tok_s, m, row);
       const int ctx = a.ctx ? __ldg(a.ctx + base + i) : 0, pos = ctx + (row - tok_s[i]);
       if (a.pos) a.pos[row] = pos;
@@ -205,7 +208,10 @@ __global__ void __launch_bounds__(kTabThreads) batch_tables_kernel(TableArgs a) 
       }
     }
     // new pages to the table, spread over all CTAs
-    for (int p = p_lo + blockIdx.x * kTabThreads + tid; p < p_hi; p += gridDim.x * kTabThreads) {
+    // (32-bit counters without a sign here and above: a last step may pass 2^31)
+    for (uint32_t u = p_lo + blockIdx.x * kTabThreads + tid; u < (uint32_t)p_hi;
+         u += gridDim.x * kTabThreads) {
+      const int p = (int)u;
       const int i = last_at_most(page_s, m, p);
       const int ctx = a.ctx ? __ldg(a.ctx + base + i) : 0;
       const int held = (int)a.pages((uint32_t)ctx + a.page - 1);
@@ -234,6 +240,7 @@ extern "C" int gdn_batch_tables(const int32_t* ctx_lens, const int32_t* new_lens
   if (num_reqs > 0 && (!new_lens || (!slot_idx && num_slots < num_reqs))) return GDN_ERR_INVALID_ARG;
   if (num_reqs > 0 && max_pages > 0 && num_slots > 0 && !page_table) return GDN_ERR_INVALID_ARG;
   if (num_free > 0 && !free_pages) return GDN_ERR_INVALID_ARG;
+  if (num_reqs > (1 << 30)) return GDN_ERR_UNSUPPORTED;  // 32-bit request indices
   const void* ptrs[] = {ctx_lens,   new_lens,  slot_idx, page_table,    free_pages, free_head,
                         cu_seqlens, positions, slot_map, free_head_out, dev_status};
   for (const void* p : ptrs)

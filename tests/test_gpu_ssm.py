@@ -390,3 +390,27 @@ def test_non_finite_b_or_c_reaches_its_group_from_its_token_on(what):
         assert not torch.any(torch.isfinite(S[1, 2:]))
         keep[1, 2:] = False
     assert torch.equal(S[keep], clean[1][keep])
+
+
+@pytest.mark.parametrize("lens", [
+    (300,) + (5, 0, 140) * 10 + (257,),          # 32 sequences, the most taken longest first
+    (129,) + (0, 7, 260) * 11,                   # 34
+    (3,) * 100 + (400,) + (0, 1) * 30 + (130,),  # 162: more than are looked at at once
+], ids=["32", "34", "162"])
+def test_prefill_of_many_sequences_in_segments(lens):
+    shape = (2, 1, 64, 128)
+    i = U.inputs(*shape, lens, BF, seed=35)
+    U.check_layer(prefill(i, gdn.SsmDims(*shape)), U.layer(i, *shape), BF, str(len(lens)))
+
+
+def test_workspace_of_a_larger_batch():
+    # sized once for the largest batch, used for others, with what those before left in it
+    shape = (4, 2, 64, 128)
+    dims = gdn.SsmDims(*shape)
+    ensure_built()
+    ws = torch.full((gdn.ssm_prefill_workspace_size(9, 1500, BF, dims),), 0x7f,
+                    dtype=torch.uint8, device="cuda")
+    for lens in ((1500,), (700, 0, 3, 130, 1, 1, 1, 600, 64), (129,)):
+        i = U.inputs(*shape, lens, BF, seed=36)
+        got, want = prefill(i, dims, workspace=ws), prefill(i, dims)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

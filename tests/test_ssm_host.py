@@ -149,3 +149,32 @@ def test_binding_refusals(L):
         gdn.batch_tables(i(0, 0), i(1, 2), None, torch.zeros(4).int(), i(1), i(0), 64, 3)
     with pytest.raises(TypeError, match="new_lens must be"):
         gdn.batch_tables(i(0), torch.ones(1), i(0), torch.zeros(1, 2).int(), i(1), i(0), 64, 1)
+
+
+def test_workspace_grows_with_the_batch(L):
+    # one workspace, sized for the largest batch, takes every smaller one
+    f = L.gdn_ssm_prefill_workspace_size
+    for dims in (ref(), ref(num_heads=32, num_groups=16, head_dim=128), ref(num_groups=1),
+                 ref(num_heads=4, num_groups=4), ref(num_heads=1024, num_groups=1, head_dim=128)):
+        for dtype in (0, 1):
+            for T in (0, 1, 127, 128, 5000, 40677, 65536, 1 << 20):
+                for n0, n1 in ((1, 2), (2, 8), (8, 96), (96, 5000)):
+                    assert f(dims, dtype, n0, T) <= f(dims, dtype, n1, T)
+                for N in (1, 2, 8):
+                    assert f(dims, dtype, N, T) <= f(dims, dtype, N, T + 129)
+    big = (1 << 31) - 1
+    assert f(ref(num_heads=1024, num_groups=1), 1, 1 << 25, 0) > 0
+    assert f(ref(), 1, big, big) > f(ref(), 1, big, 0) > 0
+
+
+def test_rows_of_x_have_the_layer_channels():
+    d = gdn.SsmDims(2, 1)
+    x, dt, a, w = torch.zeros(1, 7, d.channels), torch.zeros(7, 2), torch.zeros(2), torch.zeros(1)
+    cu = torch.tensor([0, 7], dtype=torch.int32)
+    for bad in (x, x[0, :, :-1], x[0, 0]):
+        with pytest.raises(ValueError, match="x holds"):
+            gdn.ssm_prefill(bad, dt, a, cu, w, dims=d)
+        with pytest.raises(ValueError, match="x holds"):
+            gdn.ssm_prefill_slots(bad, dt, a, cu, None, w, dims=d)
+        with pytest.raises(ValueError, match="x holds"):
+            gdn.ssm_decode_step(bad, dt, a, None, None, w, dims=d)
