@@ -1340,25 +1340,45 @@ namespace {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Chunks per segment.  A CTA works on 128 channels of one segment, so a call has pairs x units
-// CTAs, one per SM.  One sequence: as many units as fill whole waves of the GPU, with the least
-// total of chunks one after the other.  Several (whose lengths only the device knows): an SM's even
-// share of the chunks, so that a sequence is cut only if it alone would keep its SMs longer than
-// the whole call should take; every other cut costs a second conv and state update.  8 sequences of
-// 20 to 56 chunks (bf16, 64 heads of 64): a call took 1209 us with up to 4 waves and the units in
-// order, and takes 966 us so.
+// Chunks per segment.  A CTA works on 128 channels of one segment, so a call has pairs x units CTAs,
+// one per SM, the longest first.
+// One sequence: the length with the least time, counted in chunks of main: a CTA's chunks and half a
+// one to begin, whole segments over the SMs and then the shorter last ones, and 0.31 for a chunk of
+// the segments that seg goes over first.  Measured at 65,536 tokens of 64 heads: segments of 29
+// chunks 1895 us, of 37 2138 and of 64 2085 us, 1.13 and 1.10 times as long (the count says 1.12 and
+// 1.09); of 56, which it chooses, 1884 us.  4096 tokens of 32 heads of 128: 8 chunks 188 us, 4 210.
+// Several (whose lengths only the device knows): an SM's even share of the chunks, so that a sequence
+// is cut only if it alone would keep its SMs longer than the whole call should take; every other cut
+// costs a second conv and state update.  8 sequences of 20 to 56 chunks (bf16, 64 heads of 64): a
+// call took 1209 us with up to 4 waves and the units in order, and takes 966 us so.
 constexpr int kSms = 148, kMostWaves = 4;
+// Until the last SM is through with n CTAs of `a` and then m of `b` <= a.
+double makespan(int64_t n, double a, int64_t m, double b) {
+  const int64_t over = n % kSms, left = kSms - over, rounds = (m + left - 1) / left;
+  const double low = (double)(n / kSms) * a, high = over ? low + a : low;
+  const double even = ((double)n * a + (double)m * b) / kSms + b;
+  return std::max(high, std::min(low + (double)rounds * b, even));
+}
 int64_t ssm_segment(int N, int T, int pairs) {
-  const int64_t chunks = std::max<int64_t>(1, (int64_t)T / gdn::kL + N);
-  int64_t best = chunks, cost = INT64_MAX;
-  for (int waves = 1; waves <= (N > 1 ? 1 : kMostWaves); ++waves) {
-    const int units = kSms * waves / pairs;
-    if (units < 1) continue;
-    const int64_t seg = (chunks + units - 1) / units;
-    if (seg * waves < cost) {
-      cost = seg * waves;
+  if (N > 1) {
+    const int64_t chunks = (int64_t)T / gdn::kL + N;
+    const int units = std::max(1, kSms / pairs);
+    return (chunks + units - 1) / units;
+  }
+  const int64_t chunks = std::max<int64_t>(1, ((int64_t)T + gdn::kL - 1) / gdn::kL);
+  int64_t best = chunks;
+  double least = makespan(0, 0.0, pairs, chunks + 0.5);
+  for (int quarters = 5; quarters <= 4 * (kSms * kMostWaves / pairs); ++quarters) {
+    const int64_t seg = (4 * chunks + quarters - 1) / quarters;
+    if (seg >= chunks) continue;
+    const int64_t whole = chunks / seg, rest = chunks % seg;
+    const double time = makespan(whole * pairs, seg + 0.5, rest ? pairs : 0, rest + 0.5) +
+                        0.31 * makespan((whole - (rest ? 0 : 1)) * pairs, seg + 0.5, 0, 0.0);
+    if (time < least) {
+      least = time;
       best = seg;
     }
+    if (seg == 1) break;
   }
   return best;
 }
