@@ -467,22 +467,36 @@ static cudaError_t launch_ssm_prefill(bool bf16, const gdn::SsmArgs& a, int NS, 
 // outputs are in shared memory).
 static int step_blocks(int H, int G, int P) { return (H / G) * (P / gdn::kScanRows); }
 constexpr int kStepCluster = 8, kStepMost = 128;
-// CTAs per group: enough to give each of 148 SMs its four CTAs twice over.  Once over, 83 sequences of
-// 32 heads of 128 x 128 take 72 us and not 62; four times over, 128 of them 93 us and not 89 (more
-// CTAs repeat the conv of B and C more often, fewer leave SMs without work at the end).
-constexpr int kStepCtas = 148 * 4 * 2;
-static int step_cluster(int N, int G, int R) {
-  int cl = 1;
-  while (cl < kStepCluster && cl < R &&
-         ((int64_t)N * G * cl < kStepCtas || (R + cl - 1) / cl > kStepMost))
-    cl *= 2;
-  return std::min(cl, R);
+// CTAs per group (R blocks of 64 rows), by the time in us that N sequences take: 148 SMs hold four
+// CTAs each; a block of `bytes` (in and out) takes a CTA that is alone its latency, and all of them
+// together the memory bandwidth; every wave costs 2 us to begin.  Measured at 83 sequences of 48 heads
+// of 64 x 128 in one group, state in bf16: 8 CTAs (a second wave of 72) 36.9 us, 6 32.8, 4 34.8, 2
+// 43.0, 1 63.5; 128 sequences of 24 heads of 64 x 64 in two groups: 8 CTAs 36.9 us, 2 26.6, 1 32.8;
+// 256 of 32 heads of 128 x 128 in 16 groups: 1 184 us, 2 201, 4 238.
+static int step_cluster(int N, int G, int R, size_t bytes) {
+  constexpr int kSlots = 148 * 4;
+  const double latency = 0.55 + 2e-5 * bytes, shared = bytes / 6.5e6;
+  int best = std::min(kStepCluster, R);
+  double least = 1e30;
+  for (int cl = 1; cl <= kStepCluster && cl <= R; ++cl) {
+    const int nb = (R + cl - 1) / cl;
+    if (nb > kStepMost || (cl - 1) * nb >= R) continue;  // (the latter: a CTA without a block)
+    const int64_t ctas = (int64_t)N * G * cl, full = ctas / kSlots, part = ctas % kSlots;
+    const double time = full * (2.0 + nb * std::max(latency, kSlots * shared)) +
+                        (part ? 2.0 + nb * std::max(latency, part * shared) : 0.0);
+    if (time <= least * 1.001) {  // of equal ones the most CTAs: they hide one another's start
+      least = time;
+      best = cl;
+    }
+  }
+  return best;
 }
 
 template <typename T, typename TS>
 static cudaError_t launch_step(const gdn::SsmArgs& a, int NS, const char* name, cudaStream_t s) {
   const int R = step_blocks(a.H, a.G, a.P);
-  const int cl = step_cluster(a.N, a.G, R), nb = (R + cl - 1) / cl;
+  const int cl = step_cluster(a.N, a.G, R, 2 * sizeof(TS) * gdn::kScanRows * NS);
+  const int nb = (R + cl - 1) / cl;
   const dim3 grid((unsigned)a.N * a.G * cl);
   const size_t smem = (2 * NS + (gdn::kScanRows + 2) * nb) * sizeof(float);
   return NS == 128 ? launch_ssm(name, false, cl, gdn::ssm_step_kernel<T, TS, 128>, grid, smem, s, a,

@@ -414,3 +414,26 @@ def test_workspace_of_a_larger_batch():
         i = U.inputs(*shape, lens, BF, seed=36)
         got, want = prefill(i, dims, workspace=ws), prefill(i, dims)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("batch", [1, 40, 83, 150])
+@pytest.mark.parametrize("shape", [(48, 1, 64, 128), (24, 2, 64, 64), (7, 1, 128, 128)], ids=str)
+def test_decode_of_other_batches_has_the_same_bits(shape, batch):
+    # how many CTAs share a group goes by the batch; the sums of a row do not
+    H, G, P, N = shape
+    dims = gdn.SsmDims(*shape)
+    i = U.inputs(*shape, (1,) * batch, BF, seed=37)
+    S, c = dev(i["S0"]), dev(i["conv0"])
+    ensure_built()
+
+    def step(n, k):  # sequences n .. n + k - 1
+        s, h = S[n:n + k].clone(), c[n:n + k].clone()
+        o = gdn.ssm_decode_step(dev(i["x"][n:n + k]), dev(i["dt"][n:n + k]), dev(i["a_log"]), h, s,
+                                dev(i["conv_w"]), conv_b=dev(i["conv_b"]), D=dev(i["D"]),
+                                z=dev(i["z"][n:n + k]), dims=dims)
+        return o, s, h
+
+    o, s, h = step(0, batch)
+    for n in sorted({0, batch // 2, batch - 1}):
+        for got, one in zip((o, s, h), step(n, 1)):
+            assert torch.equal(got[n:n + 1], one)
