@@ -342,6 +342,12 @@ int gdn_decode_step_bf16_state(const gdn_dims* dims, gdn_dtype dtype, const void
  * device memory (cu_seqlens, slot_idx) is checked on the device in every build: a sequence whose
  * cu_seqlens entries are out of order or past num_tokens counts as empty and sets dev_status to
  * GDN_ERR_INVALID_ARG.  Rows of `out` at and behind cu[N] are left as they were.
+ * Precision: fp32 sums and states throughout.  Prompts in bf16 go chunk by chunk (128 tokens)
+ * through fp16 operands with power-of-two row scales: outputs are within 2^-10 + 2^-13 of the sum
+ * of the magnitudes of what forms them (and rounded to bf16), the fp32 state within 2^-14 of it.
+ * NaN and infinity reach only outputs from their token on.  A NaN or infinity among the conv
+ * outputs of x makes, in a bf16 prompt, the head's 64 channels around it NaN (channels 0-63 or
+ * 64-127), and one in B all states of its group; single tokens and fp32 prompts follow the formula.
  */
 typedef struct gdn_ssm_dims {
   int32_t num_heads;   /* H: a multiple of num_groups */
