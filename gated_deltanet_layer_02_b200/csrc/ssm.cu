@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 #include <utility>
 
 #include "args.cuh"
@@ -17,12 +18,11 @@ namespace gdn {
 
 constexpr int kScanThreads = 128;
 constexpr int kScanRows = 64;   // rows of the state per CTA (16 per warp, 8 lanes per row)
-constexpr int kConvRun = 16;    // tokens per thread of the packed conv
+constexpr int kConvRun = 4;    // tokens per thread of the packed conv
 
 // Packed prompts: a thread owns 8 channels and a run of kConvRun tokens, the three rows before
 // the current one in registers.
 __global__ void __launch_bounds__(128) ssm_conv_kernel(SsmArgs a) {
-  pdl_trigger();
   const int c = (blockIdx.y * 128 + threadIdx.x) * 8, t0 = blockIdx.x * kConvRun;
   if (c >= a.Cc) return;
   float w[4][8], b[8];
@@ -116,13 +116,12 @@ struct Raw<__nv_bfloat16> {
   }
 };
 
-// One token of Q quads: the rows take alpha S + dx B^T; o: S C of the lane's row of each quad, in
-// every lane of its group of eight.  B, C: the lane's first column.
+// One token of Q quads: the rows take alpha S + dx B^T; o: this lane's share of S C of its row of each
+// quad (see ssm_rows_sum).  B, C: the lane's first column.
 template <int Q, int M>
 __device__ __forceinline__ void ssm_rows_step(float4 (&f)[Q][M], const float* B, const float* C,
                                               const float (&dx)[Q], float alpha, float (&o)[Q]) {
-#pragma unroll
-  for (int q = 0; q < Q; ++q) o[q] = 0.f;
+  float p[Q][2] = {};  // two sums: half as long a chain
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     const float4 b = *reinterpret_cast<const float4*>(B + 32 * m);
@@ -134,9 +133,16 @@ __device__ __forceinline__ void ssm_rows_step(float4 (&f)[Q][M], const float* B,
       r.y = fmaf(alpha, r.y, dx[q] * b.y);
       r.z = fmaf(alpha, r.z, dx[q] * b.z);
       r.w = fmaf(alpha, r.w, dx[q] * b.w);
-      o[q] = fmaf(r.x, c.x, fmaf(r.y, c.y, fmaf(r.z, c.z, fmaf(r.w, c.w, o[q]))));
+      p[q][0] = fmaf(r.x, c.x, fmaf(r.y, c.y, p[q][0]));
+      p[q][1] = fmaf(r.z, c.z, fmaf(r.w, c.w, p[q][1]));
     }
   }
+#pragma unroll
+  for (int q = 0; q < Q; ++q) o[q] = p[q][0] + p[q][1];
+}
+// Sums over the eight lanes of a row, in all of them.
+template <int Q>
+__device__ __forceinline__ void ssm_rows_sum(float (&o)[Q]) {
 #pragma unroll
   for (int off = 4; off > 0; off >>= 1)
 #pragma unroll
@@ -146,7 +152,9 @@ __device__ __forceinline__ void ssm_rows_step(float4 (&f)[Q][M], const float* B,
 // ------------------------------------------------------------------------- packed prompts, fp32
 // Tokens of a sequence come kScanBlock at a time to shared memory (B, C, the CTA's channels of x and
 // z, step and decay), the next ones in flight while these are worked through; y takes the place of
-// x and leaves a block at a time.  A CTA has 16 Q rows of a head's state, 4 Q per warp.
+// x and leaves a block at a time.  A CTA has 16 Q rows of a head's state, 4 Q per warp.  A sequence is
+// a chain of tokens, so latency bounds it: a warp takes 8 tokens (2 with Q = 4) at a time, whose sums
+// over lanes overlap, 0.22 us per token of one sequence of 1021 (one at a time: 0.29).
 constexpr int kScanBlock = 16;
 template <int NS, int Q>
 struct ScanTokens {
@@ -216,7 +224,6 @@ __global__ void __launch_bounds__(kScanThreads, 4) ssm_scan_kernel(SsmArgs a) {
       b.gate[tid] = make_float2(d, expf(rate * d));
     }
   };
-  pdl_wait();  // the conv outputs
   if (s < end) fetch(s, buf[0]);
   for (int t0 = s, k = 0; t0 < end; t0 += kScanBlock, k ^= 1) {
     if (t0 + kScanBlock < end) {
@@ -228,21 +235,35 @@ __global__ void __launch_bounds__(kScanThreads, 4) ssm_scan_kernel(SsmArgs a) {
     __syncthreads();
     Tokens& b = buf[k];
     const int m = min(kScanBlock, end - t0);
-#pragma unroll 2
-    for (int i = 0; i < m; ++i) {
-      float xv[Q], dx[Q], o[Q];
-      const float2 gt = b.gate[i];
+    // U tokens, whose sums over lanes are independent and whose results leave together
+    auto tokens = [&](int i, auto count) {
+      constexpr int U = decltype(count)::value;
+      float xv[U][Q], o[U * Q];
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        xv[q] = b.x[i][r0 + 4 * q];
-        dx[q] = gt.x * xv[q];
+      for (int u = 0; u < U; ++u) {
+        const float2 gt = b.gate[i + u];
+        float dx[Q], part[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          xv[u][q] = b.x[i + u][r0 + 4 * q];
+          dx[q] = gt.x * xv[u][q];
+        }
+        ssm_rows_step(f, &b.B[i + u][4 * sub], &b.C[i + u][4 * sub], dx, gt.y, part);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) o[u * Q + q] = part[q];
       }
-      ssm_rows_step(f, &b.B[i][4 * sub], &b.C[i][4 * sub], dx, gt.y, o);
+      ssm_rows_sum(o);
       if (sub == 0) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) b.x[i][r0 + 4 * q] = fmaf(D, xv[q], o[q]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int q = 0; q < Q; ++q) b.x[i + u][r0 + 4 * q] = fmaf(D, xv[u][q], o[u * Q + q]);
       }
-    }
+    };
+    constexpr int U = Q == 1 ? 8 : 2;
+    int i = 0;
+    for (; i + U <= m; i += U) tokens(i, std::integral_constant<int, U>());
+    for (; i < m; ++i) tokens(i, std::integral_constant<int, 1>());
     __syncthreads();
     for (int v = tid; v < m * (kRows / 4); v += kScanThreads) {
       const int t = v / (kRows / 4), p = 4 * (v % (kRows / 4));
@@ -364,6 +385,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) ssm_step_kernel(SsmArgs a, in
       for (int m = 0; m < M; ++m) f[q][m] = cur[q][m].get();
     }
     ssm_rows_step(f, B_s + 4 * sub, C_s + 4 * sub, dx, gt.x, o);
+    ssm_rows_sum(o);
     TS* p = S + ((size_t)b * kScanRows + (bt % kBatches) * (4 * Q)) * NS;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
@@ -400,27 +422,19 @@ __global__ void __launch_bounds__(kScanThreads, 4) ssm_step_kernel(SsmArgs a, in
 namespace gdn_host {
 
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_ssm(const char* name, bool pdl, int cluster, void (*kern)(KArgs...),
+static cudaError_t launch_ssm(const char* name, int cluster, void (*kern)(KArgs...),
                               dim3 grid, size_t smem, cudaStream_t s, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (pdl && !trace_attached()) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = cluster;
-    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-    ++n;
-  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = n;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
   trace_begin(name, s);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
   trace_end(s);
@@ -432,14 +446,15 @@ size_t ssm_tc_workspace(int N, int T, int H, int G, int P, int NS, int Cc);
 
 template <int NS, int Q>
 static cudaError_t launch_scan(const gdn::SsmArgs& a, cudaStream_t s) {
-  const bool pdl = a.T > 0;  // behind a conv of this call; alone, it is an ordinary launch
   const size_t smem = 2 * sizeof(gdn::ScanTokens<NS, Q>);
   if (smem > 48 * 1024) {  // per call, not once: the attribute belongs to the current device
     const cudaError_t e = cudaFuncSetAttribute(
         gdn::ssm_scan_kernel<NS, Q>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_ssm("ssm_scan", pdl, 1, gdn::ssm_scan_kernel<NS, Q>,
+  // Not before the conv has ended: CTAs that start while it runs share the SMs it has left, and the
+  // recurrence takes as long as its slowest SM (1021 tokens in three sequences: 191 us and not 106).
+  return launch_ssm("ssm_scan", 1, gdn::ssm_scan_kernel<NS, Q>,
                     dim3((unsigned)a.N * a.H * (a.P / (16 * Q))), smem, s, a);
 }
 
@@ -452,13 +467,14 @@ static cudaError_t launch_ssm_prefill(bool bf16, const gdn::SsmArgs& a, int NS, 
   }
   if (a.T > 0) {
     const dim3 grid((a.T + gdn::kConvRun - 1) / gdn::kConvRun, (a.Cc / 8 + 127) / 128);
-    cudaError_t e = launch_ssm("ssm_conv", false, 1, gdn::ssm_conv_kernel, grid, 0, s, a);
+    cudaError_t e = launch_ssm("ssm_conv", 1, gdn::ssm_conv_kernel, grid, 0, s, a);
     if (e != cudaSuccess) return e;
   }
-  // Rows per CTA: 16 where that is needed to have work for all SMs (a token costs one quad per warp
-  // and not four: 1000 tokens of two sequences of 64 heads of 64 x 128 take 350 us and not 525), 64
-  // else (B and C are read for four quads at once: eight such sequences 178 us and not 243).
-  if ((int64_t)a.N * a.H * (a.P / 64) < 2 * 148)
+  // Rows per CTA: 16 while 64 would leave SMs without work (a token then costs a warp one quad and
+  // not four), else 64 (B and C are read for four quads at once).  16 and 64 rows: three sequences of
+  // 1021 tokens in all, 4 heads of 128 x 128, 105 and 180 us; 1000 tokens of 64 heads of 64 x 128 in
+  // two sequences 265 and 270, in four 223 and 185, in eight 218 and 152.
+  if ((int64_t)a.N * a.H * (a.P / 64) <= 148)
     return NS == 128 ? launch_scan<128, 1>(a, s) : launch_scan<64, 1>(a, s);
   return NS == 128 ? launch_scan<128, 4>(a, s) : launch_scan<64, 4>(a, s);
 }
@@ -499,9 +515,9 @@ static cudaError_t launch_step(const gdn::SsmArgs& a, int NS, const char* name, 
   const int nb = (R + cl - 1) / cl;
   const dim3 grid((unsigned)a.N * a.G * cl);
   const size_t smem = (2 * NS + (gdn::kScanRows + 2) * nb) * sizeof(float);
-  return NS == 128 ? launch_ssm(name, false, cl, gdn::ssm_step_kernel<T, TS, 128>, grid, smem, s, a,
+  return NS == 128 ? launch_ssm(name, cl, gdn::ssm_step_kernel<T, TS, 128>, grid, smem, s, a,
                                 cl, nb)
-                   : launch_ssm(name, false, cl, gdn::ssm_step_kernel<T, TS, 64>, grid, smem, s, a,
+                   : launch_ssm(name, cl, gdn::ssm_step_kernel<T, TS, 64>, grid, smem, s, a,
                                 cl, nb);
 }
 
