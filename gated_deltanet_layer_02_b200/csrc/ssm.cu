@@ -192,6 +192,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) ssm_scan_kernel(SsmArgs a) {
   const int cB = a.H * a.P + (h / (a.H / a.G)) * NS, cC = cB + a.G * NS;
   const int cx = h * a.P + pb * kRows;
   // 16-byte pieces of a token: NS / 4 of B, as many of C, 4 Q of x, 4 Q of z
+  const bool gates = tid < kScanBlock;
+  auto load_dt = [&](int t) { return gates && t < end ? a.dt[(size_t)t * a.H + h] : 0.f; };
+  float raw = load_dt(s + tid);  // of the block that is fetched next
   auto fetch = [&](int t0, Tokens& b) {
     constexpr int kBC = NS / 4, kX = kRows / 4, kPieces = 2 * kBC + 2 * kX;
     for (int v = tid; v < kScanBlock * kPieces; v += kScanThreads) {
@@ -219,9 +222,10 @@ __global__ void __launch_bounds__(kScanThreads, 4) ssm_scan_kernel(SsmArgs a) {
                    : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    if (tid < kScanBlock && t0 + tid < end) {
-      const float d = ssm_step(a.dt[(size_t)(t0 + tid) * a.H + h] + bias, a.dt_min, a.dt_max);
+    if (gates) {
+      const float d = ssm_step(raw + bias, a.dt_min, a.dt_max);
       b.gate[tid] = make_float2(d, expf(rate * d));
+      raw = t0 + tid < end - kScanBlock ? load_dt(t0 + kScanBlock + tid) : 0.f;
     }
   };
   if (s < end) fetch(s, buf[0]);
