@@ -154,10 +154,11 @@ __device__ __forceinline__ void ssm_rows_sum(float (&o)[Q]) {
 // z, step and decay), the next ones in flight while these are worked through; y takes the place of
 // x and leaves a block at a time.  A CTA has 16 Q rows of a head's state, 4 Q per warp.  A sequence is
 // a chain of tokens, so latency bounds it: a warp takes 8 tokens (2 with Q = 4) at a time, whose sums
-// over lanes overlap, 0.22 us per token of one sequence of 1021 (one at a time: 0.29).
-constexpr int kScanBlock = 16;
+// over lanes overlap (one sequence of 1021 tokens: 0.29 us per token one at a time, 0.22 so), and a
+// block is 32 tokens where few CTAs leave room for it (three sequences: 99 us with 16, 91 with 32).
 template <int NS, int Q>
 struct ScanTokens {
+  static constexpr int kScanBlock = Q == 1 ? 32 : 16;
   float B[kScanBlock][NS], C[kScanBlock][NS], x[kScanBlock][16 * Q], z[kScanBlock][16 * Q];
   float2 gate[kScanBlock];  // step, decay
 };
@@ -166,7 +167,7 @@ template <int NS, int Q>
 __global__ void __launch_bounds__(kScanThreads, 4) ssm_scan_kernel(SsmArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   using Tokens = ScanTokens<NS, Q>;
-  constexpr int kRows = 16 * Q, M = NS / 32;
+  constexpr int kRows = 16 * Q, M = NS / 32, kScanBlock = Tokens::kScanBlock;
   Tokens* buf = reinterpret_cast<Tokens*>(smem);  // [2]
   const int blocks = a.P / kRows;
   const int pb = blockIdx.x % blocks, h = (blockIdx.x / blocks) % a.H;
@@ -474,11 +475,11 @@ static cudaError_t launch_ssm_prefill(bool bf16, const gdn::SsmArgs& a, int NS, 
     cudaError_t e = launch_ssm("ssm_conv", 1, gdn::ssm_conv_kernel, grid, 0, s, a);
     if (e != cudaSuccess) return e;
   }
-  // Rows per CTA: 16 while 64 would leave SMs without work (a token then costs a warp one quad and
-  // not four), else 64 (B and C are read for four quads at once).  16 and 64 rows: three sequences of
-  // 1021 tokens in all, 4 heads of 128 x 128, 105 and 180 us; 1000 tokens of 64 heads of 64 x 128 in
-  // two sequences 265 and 270, in four 223 and 185, in eight 218 and 152.
-  if ((int64_t)a.N * a.H * (a.P / 64) <= 148)
+  // Rows per CTA: 16 while all CTAs are resident at once, three to an SM (a token costs a warp one
+  // quad and not four, and a block of tokens may be twice as long), else 64 (B and C are read for four
+  // quads at once).  16 and 64 rows: three sequences of 1021 tokens in all, 4 heads of 128 x 128, 91
+  // and 180 us; 1000 tokens of 64 heads of 64 x 128 in two sequences 283 and 266, in four 223 and 183.
+  if ((int64_t)a.N * a.H * (a.P / 64) * 4 <= 3 * 148)
     return NS == 128 ? launch_scan<128, 1>(a, s) : launch_scan<64, 1>(a, s);
   return NS == 128 ? launch_scan<128, 4>(a, s) : launch_scan<64, 4>(a, s);
 }
