@@ -933,7 +933,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(const __grid_constant__
 // TMEM, per pipeline: what the chunk adds to S^T (64 columns), C S^T and P X (128), P (64).  S^T
 // itself stays in registers (32 of a row per thread): fp32 sums there round to nearest.
 // Bound by the chain of a chunk's phases (conv, scales, weights, products, epilogue): 8 to 9 us for
-// one pipeline alone, 10.8 for the two, with 38 % of issue slots and 8 % of the tensor pipe busy.
+// one pipeline alone, 10.8 for the two, with 39 % of issue slots and 9 % of the tensor pipe busy.
 // 4096 tokens of 32 heads of 128 102 us, 65,536 of 64 heads of 64 1213 us, 40,677 in eight 926 us.
 constexpr uint32_t kMainPipe = 6 * kTileB, kMainCtl = kMainPipe + 8 * kTileB;
 constexpr uint32_t kMainSmem = kMainCtl + 3072;
