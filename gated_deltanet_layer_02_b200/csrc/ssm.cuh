@@ -78,7 +78,7 @@ __device__ __forceinline__ void conv_history(const SsmArgs& a, int n, int row, i
 struct SsmTcArgs {
   SsmArgs a;
   uint8_t* tiles;        // C, B high, B low (fp16): [128][128] each, as swizzled row tiles
-  __half* cb;            // [128][128] C B^T, blocks of 32 columns up to the diagonal
+  __half* cb;            // [128][128] C B^T (see cb_off), blocks of 32 columns up to the diagonal
   int8_t* ex;            // [2][128] exponents of the rows of B and of C
   __nv_bfloat16* hist;   // [N][3][Cc] initial conv history (NULL: zeros)
   float* gate;           // per chunk and head: [3][128] w, log2(delta) - cum, cum (see gates)

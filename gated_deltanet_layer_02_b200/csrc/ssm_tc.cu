@@ -338,6 +338,10 @@ __device__ __forceinline__ Unit find_unit_by_length(const SsmArgs& a, int seg, i
               uniform(it ? r.e : 0),  uniform(it ? r.chunk : 0), uniform(it ? r.first : 0)};
 }
 
+// C B^T in memory: for 32 rows, a block of 32 columns and a half of it, 16 columns of each row after
+// one another, so that a warp (a row per lane) reads and writes 1 KB in one piece.
+__device__ __forceinline__ int cb_off(int blk, int half) { return (blk * 2 + half) * 32 * 16; }
+
 // ------------------------------------------------------------------------------------- bc
 // 512 threads: warp w has tokens 8 w .. 8 w + 7 of the chunk, first of B, then of C; a lane holds 4
 // channels of a row.  State widths below 128 are padded with zero channels.
@@ -542,8 +546,7 @@ __global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ 
   tc_fence_after();
   if (!ok && tid == 0) report_status(a.status, GDN_ERR_TIMEOUT);
   // rows of the product: the blocks of 32 columns up to the diagonal
-  const int i = (warp & 3) * 32 + lane;
-  __half* cb = g.cb + (at * kL + i) * kL;
+  __half* cb = g.cb + (at * kL + (warp & 3) * 32) * kL + lane * 16;
   {
     const int blk = warp >> 2;
     if (blk <= (warp & 3)) {
@@ -551,13 +554,17 @@ __global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ 
     tmem_ld32(tmem_at(tmem, (warp & 3) * 32, blk * 32), v);
     tmem_ld_wait();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint4 f;
-      f.x = pack_f16x2(mul2(make_float2(v[8 * q], v[8 * q + 1]), pow2(kScaleCB)));
-      f.y = pack_f16x2(mul2(make_float2(v[8 * q + 2], v[8 * q + 3]), pow2(kScaleCB)));
-      f.z = pack_f16x2(mul2(make_float2(v[8 * q + 4], v[8 * q + 5]), pow2(kScaleCB)));
-      f.w = pack_f16x2(mul2(make_float2(v[8 * q + 6], v[8 * q + 7]), pow2(kScaleCB)));
-      *reinterpret_cast<uint4*>(cb + blk * 32 + 8 * q) = f;
+    for (int q = 0; q < 4; q += 2) {
+      uint4 f[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const float* w = v + 8 * (q + p);
+        f[p].x = pack_f16x2(mul2(make_float2(w[0], w[1]), pow2(kScaleCB)));
+        f[p].y = pack_f16x2(mul2(make_float2(w[2], w[3]), pow2(kScaleCB)));
+        f[p].z = pack_f16x2(mul2(make_float2(w[4], w[5]), pow2(kScaleCB)));
+        f[p].w = pack_f16x2(mul2(make_float2(w[6], w[7]), pow2(kScaleCB)));
+      }
+      store32(cb + cb_off(blk, q >> 1), f[0], f[1]);
     }
     }
   }
@@ -984,6 +991,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
   const int row = uniform(state_row(a.slot, un.n, a.num_slots));
   if (row < 0 && tid == 0) report_status(a.status, GDN_ERR_INVALID_ARG);
   const float D = a.D ? a.D[s.h] : 0.f;
+  const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
   const int quad = pw & 3, half = pw >> 2;
   const int i = quad * 32 + lane;   // row of this thread: token of the chunk, or n of the state
   const int p0 = half * 32;         // its channels
@@ -1151,13 +1159,12 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
       }
       // C B^T of this thread's columns: 16 of each block of 32 up to the diagonal
       // (two blocks ahead)
-      const __half* cb = g.cb + (at * kL + i) * kL + half * 16;
+      const __half* cb = g.cb + (at * kL + quad * 32) * kL + lane * 16;
       uint4 cbr[2][2];
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
         if (blk <= quad) {
-          cbr[blk][0] = ldg128(cb + blk * 32);
-          cbr[blk][1] = ldg128(cb + blk * 32 + 8);
+          load32_nc(cb + cb_off(blk, half), cbr[blk][0], cbr[blk][1]);
         }
       }
       fence_proxy_async_smem();
@@ -1196,8 +1203,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
             const uint4 r0 = cbr[blk & 1][0], r1 = cbr[blk & 1][1];
             const uint32_t in[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
             if (blk + 2 <= quad) {
-              cbr[blk & 1][0] = ldg128(cb + (blk + 2) * 32);
-              cbr[blk & 1][1] = ldg128(cb + (blk + 2) * 32 + 8);
+              load32_nc(cb + cb_off(blk + 2, half), cbr[blk & 1][0], cbr[blk & 1][1]);
             }
             uint32_t out[8];
             const int j0 = blk * 32 + half * 16;
@@ -1274,6 +1280,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
       if (k + 1 < nch) load_x(g, un, s, t0 + kL, warp, lane, S16, halo);
       __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + o_at;
       smax = 0.f;
+      uint4 even = {};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         float yi[8], yx[8], add[8];
@@ -1306,7 +1313,17 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
             if (a.z) y = __fmul2_rn(y, silu2(unpack_bf16x2(zw[e])));
             ow[e] = pack_bf16x2(y.x, y.y);
           }
-          *reinterpret_cast<uint4*>(op + 8 * r) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+          // two quarters leave together, as whole sectors where the output allows it (40,677 tokens
+          // in eight sequences: 868 us and not 924)
+          const uint4 now = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+          if ((r & 1) == 0) {
+            even = now;
+          } else if (out32) {
+            store32(op + 8 * (r - 1), even, now);
+          } else {
+            *reinterpret_cast<uint4*>(op + 8 * (r - 1)) = even;
+            *reinterpret_cast<uint4*>(op + 8 * r) = now;
+          }
         }
       }
       tc_fence_before();

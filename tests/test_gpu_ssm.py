@@ -437,3 +437,17 @@ def test_decode_of_other_batches_has_the_same_bits(shape, batch):
     for n in sorted({0, batch // 2, batch - 1}):
         for got, one in zip((o, s, h), step(n, 1)):
             assert torch.equal(got[n:n + 1], one)
+
+
+@pytest.mark.parametrize("off", [8, 16], ids=["16 bytes", "32 bytes"])
+def test_output_aligned_to_16_bytes(off):
+    # outputs leave 32 bytes at a time where their address allows it, 16 else: the same values
+    shape, lens = (4, 2, 64, 128), (130, 3, 200)
+    dims = gdn.SsmDims(*shape)
+    i = U.inputs(*shape, lens, BF, seed=38)
+    want = prefill(i, dims)[0]
+    buf = torch.full((want.numel() + 2 * off,), 7.0, dtype=BF, device="cuda")
+    out = buf[off:off + want.numel()].view_as(want)
+    prefill(i, dims, out=out)
+    assert torch.equal(out, want)
+    assert torch.all(buf[:off] == 7.0) and torch.all(buf[-off:] == 7.0)
