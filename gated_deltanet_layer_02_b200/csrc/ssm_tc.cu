@@ -991,7 +991,18 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
   const int row = uniform(state_row(a.slot, un.n, a.num_slots));
   if (row < 0 && tid == 0) report_status(a.status, GDN_ERR_INVALID_ARG);
   const float D = a.D ? a.D[s.h] : 0.f;
-  const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+  // whole sectors of z and of the output, where their addresses allow it (40,677 tokens in eight
+  // sequences: 799 us; with z in 16-byte pieces 822)
+  const bool wide =
+      ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.z)) & 31u) == 0;
+  auto load_z = [&](const __nv_bfloat16* p, uint4& lo, uint4& hi) {
+    if (wide) {
+      load32_nc(p, lo, hi);
+    } else {
+      lo = ldg128(p);
+      hi = ldg128(p + 8);
+    }
+  };
   const int quad = pw & 3, half = pw >> 2;
   const int i = quad * 32 + lane;   // row of this thread: token of the chunk, or n of the state
   const int p0 = half * 32;         // its channels
@@ -1255,11 +1266,8 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
       const bool in = i < L;
       const size_t o_at = ((size_t)(t0 + i) * a.H) * a.P + s.c + p0;
       const __nv_bfloat16* zp = static_cast<const __nv_bfloat16*>(a.z) + o_at;
-      uint4 zr[2] = {};  // two quarters ahead
-      if (a.z && in) {
-        zr[0] = ldg128(zp);
-        zr[1] = ldg128(zp + 8);
-      }
+      uint4 zr[2] = {};  // of two quarters
+      if (a.z && in) load_z(zp, zr[0], zr[1]);
       const float cum = ldgf(gate + 2 * kL + i);
       const int eC = ldg8(ex + kL + i);
       const float dec = exp2f((float)__ldg(g.decay + chunk * a.H + s.h));
@@ -1301,7 +1309,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
         if (in) {
           const uint4 xr = *reinterpret_cast<const uint4*>(X + sw128_off(i, half * 4 + r));
           const uint4 zv = zr[r & 1];
-          if (r < 2 && a.z) zr[r] = ldg128(zp + 8 * (r + 2));
+          if (r == 1 && a.z) load_z(zp + 16, zr[0], zr[1]);
           const uint32_t xw[4] = {xr.x, xr.y, xr.z, xr.w};
           const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
           uint32_t ow[4];
@@ -1313,12 +1321,11 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
             if (a.z) y = __fmul2_rn(y, silu2(unpack_bf16x2(zw[e])));
             ow[e] = pack_bf16x2(y.x, y.y);
           }
-          // two quarters leave together, as whole sectors where the output allows it (40,677 tokens
-          // in eight sequences: 868 us and not 924)
+          // two quarters leave together (with 16-byte stores, in the case above, 868 us become 924)
           const uint4 now = make_uint4(ow[0], ow[1], ow[2], ow[3]);
           if ((r & 1) == 0) {
             even = now;
-          } else if (out32) {
+          } else if (wide) {
             store32(op + 8 * (r - 1), even, now);
           } else {
             *reinterpret_cast<uint4*>(op + 8 * (r - 1)) = even;

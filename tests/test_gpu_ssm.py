@@ -451,3 +451,20 @@ def test_output_aligned_to_16_bytes(off):
     prefill(i, dims, out=out)
     assert torch.equal(out, want)
     assert torch.all(buf[:off] == 7.0) and torch.all(buf[-off:] == 7.0)
+
+
+@pytest.mark.parametrize("off", [8, 16], ids=["16 bytes", "32 bytes"])
+def test_gate_aligned_to_16_bytes(off):
+    shape, lens = (4, 2, 64, 128), (130, 3, 200)
+    dims = gdn.SsmDims(*shape)
+    i = U.inputs(*shape, lens, BF, seed=38)
+    want = prefill(i, dims)[0]
+    z = dev(i["z"])
+    buf = torch.full((z.numel() + 2 * off,), float("nan"), dtype=BF, device="cuda")
+    at = buf[off:off + z.numel()].view_as(z)
+    at.copy_(z)
+    got = gdn.ssm_prefill(dev(i["x"]), dev(i["dt"]), dev(i["a_log"]), dev(i["cu"]),
+                          dev(i["conv_w"]), conv_b=dev(i["conv_b"]), dt_bias=dev(i["dt_bias"]),
+                          D=dev(i["D"]), z=at, S0=dev(i["S0"]), conv0=dev(i["conv0"]), dims=dims)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
