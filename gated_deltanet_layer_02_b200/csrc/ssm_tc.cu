@@ -458,18 +458,30 @@ __global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ 
   uint8_t* tiles = g.tiles + at * kBcBytes;
   int8_t* ex = g.ex + at * 2 * kL;
   const bool live = lane * 4 < g.NS;
+  const bool inside = t0 + i0 - 3 >= un.s && t0 + i0 + 8 <= un.e;
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {  // B, then C
     const int c = a.H * a.P + (part * a.G + grp) * g.NS + lane * 4;
     uint2 raw[11];  // the warp's rows and the three before them
-#pragma unroll
-    for (int q = 0; q < 11; ++q) {  // (row addresses are the same for the whole warp)
-      const int t = t0 + i0 + q - 3;
+    if (inside) {  // all of the sequence: no checks per row (65,536 tokens: 250 us with them, 232 without)
       const __nv_bfloat16* r =
-          t >= un.s ? static_cast<const __nv_bfloat16*>(a.x) + (size_t)t * a.Cc
-                    : (c0 && row >= 0 ? c0 + ((size_t)row * 3 + 3 + t - un.s) * a.Cc : nullptr);
-      raw[q] = make_uint2(0, 0);
-      if (r && i0 < L && t < un.e && live) raw[q] = *reinterpret_cast<const uint2*>(r + c);
+          static_cast<const __nv_bfloat16*>(a.x) + (size_t)(t0 + i0 - 3) * a.Cc + c;
+#pragma unroll
+      for (int q = 0; q < 11; ++q) {
+        raw[q] = make_uint2(0, 0);
+        if (live) raw[q] = *reinterpret_cast<const uint2*>(r);
+        r += a.Cc;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 11; ++q) {  // (row addresses are the same for the whole warp)
+        const int t = t0 + i0 + q - 3;
+        const __nv_bfloat16* r =
+            t >= un.s ? static_cast<const __nv_bfloat16*>(a.x) + (size_t)t * a.Cc
+                      : (c0 && row >= 0 ? c0 + ((size_t)row * 3 + 3 + t - un.s) * a.Cc : nullptr);
+        raw[q] = make_uint2(0, 0);
+        if (r && i0 < L && t < un.e && live) raw[q] = *reinterpret_cast<const uint2*>(r + c);
+      }
     }
     uint4 wr[2] = {};
     uint2 br = make_uint2(0, 0);
@@ -489,6 +501,10 @@ __global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ 
       w[2][p] = make_float2(wb.x, wd.x), w[3][p] = make_float2(wb.y, wd.y);
       b[p] = unpack_bf16x2(p ? br.y : br.x);
     }
+    float2 h[3][2];  // the three rows before the current one
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      h[q][0] = unpack_bf16x2(raw[q].x), h[q][1] = unpack_bf16x2(raw[q].y);
     uint32_t tops = 0;
     uint8_t* hi_out = tiles + (part ? 0 : 2 * kTileB);
 #pragma unroll
@@ -496,11 +512,12 @@ __global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ 
       float2 u[2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        auto word = [&](const uint2& r) { return unpack_bf16x2(p ? r.y : r.x); };
-        float2 y = __ffma2_rn(w[0][p], word(raw[q]), b[p]);
-        y = __ffma2_rn(w[1][p], word(raw[q + 1]), y);
-        y = __ffma2_rn(w[2][p], word(raw[q + 2]), y);
-        u[p] = silu2(__ffma2_rn(w[3][p], word(raw[q + 3]), y));
+        const float2 v = unpack_bf16x2(p ? raw[q + 3].y : raw[q + 3].x);
+        float2 y = __ffma2_rn(w[0][p], h[0][p], b[p]);
+        y = __ffma2_rn(w[1][p], h[1][p], y);
+        y = __ffma2_rn(w[2][p], h[2][p], y);
+        u[p] = silu2(__ffma2_rn(w[3][p], v, y));
+        h[0][p] = h[1][p], h[1][p] = h[2][p], h[2][p] = v;
         if (i0 + q >= L) u[p] = make_float2(0.f, 0.f);
       }
       const uint32_t top = __reduce_max_sync(
