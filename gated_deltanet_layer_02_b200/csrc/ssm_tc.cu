@@ -1390,10 +1390,10 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // Chunks per segment.  A CTA works on 128 channels of one segment, so a call has pairs x units CTAs,
 // one per SM, the longest first.
 // One sequence: the length with the least time, counted in chunks of main: a CTA's chunks and half a
-// one to begin, whole segments over the SMs and then the shorter last ones, and 0.31 for a chunk of
+// one to begin, whole segments over the SMs and then the shorter last ones, and 0.36 for a chunk of
 // the segments that seg goes over first.  Measured at 65,536 tokens of 64 heads: segments of 29
-// chunks 1895 us, of 37 2138 and of 64 2085 us, 1.13 and 1.10 times as long (the count says 1.12 and
-// 1.09); of 56, which it chooses, 1884 us.  4096 tokens of 32 heads of 128: 8 chunks 188 us, 4 210.
+// chunks 1719 us, of 37 1881 and of 64 1923 us, 1.09 and 1.12 times as long (the count says 1.11 and
+// 1.09); of 56, which it chooses, 1645 us.  4096 tokens of 32 heads of 128: 8 chunks 177 us, 4 242.
 // Several (whose lengths only the device knows): an SM's even share of the chunks, so that a sequence
 // is cut only if it alone would keep its SMs longer than the whole call should take; every other cut
 // costs a second conv and state update.  8 sequences of 20 to 56 chunks (bf16, 64 heads of 64): a
@@ -1420,7 +1420,7 @@ int64_t ssm_segment(int N, int T, int pairs) {
     if (seg >= chunks) continue;
     const int64_t whole = chunks / seg, rest = chunks % seg;
     const double time = makespan(whole * pairs, seg + 0.5, rest ? pairs : 0, rest + 0.5) +
-                        0.31 * makespan((whole - (rest ? 0 : 1)) * pairs, seg + 0.5, 0, 0.0);
+                        0.36 * makespan((whole - (rest ? 0 : 1)) * pairs, seg + 0.5, 0, 0.0);
     if (time < least) {
       least = time;
       best = seg;
