@@ -345,8 +345,8 @@ __device__ __forceinline__ int cb_off(int blk, int half) { return (blk * 2 + hal
 // ------------------------------------------------------------------------------------- bc
 // 512 threads: warp w has tokens 8 w .. 8 w + 7 of the chunk, first of B, then of C; a lane holds 4
 // channels of a row.  State widths below 128 are padded with zero channels.
-// Bound by instructions: 63 % of issue slots, 1.4 TB/s.  4096 tokens of 16 groups 38 us, 65,536 of
-// 8 groups 265 us; one chunk 15 us, of which an empty launch is 6.
+// Bound by instructions: 63 % of issue slots, 1.5 TB/s.  4096 tokens of 16 groups 36 us, 65,536 of
+// 8 groups 229 us; one chunk 14 to 17 us, of which an empty launch is 6.
 constexpr uint32_t kBcSmem = 4 * kTileB + 2048;
 constexpr int kGateHeads = 32;  // heads per gates CTA
 
@@ -767,7 +767,7 @@ __device__ __forceinline__ void store_parts(float2 u, float w, uint8_t* W, uint3
 // The state a segment adds, the sum over its tokens of 2^(log decay from the token to the
 // segment's end) delta x B^T (for the first segment: and the decayed initial state), chunk by
 // chunk from its end; the chunks' contributions are added in fp32 registers.
-// 3.3 us per chunk of 128 channels; 65,536 tokens of 64 heads of 64 388 us, half of issue slots busy.
+// 3.3 us per chunk of 128 channels; 65,536 tokens of 64 heads of 64 385 us, 55 % of issue slots busy.
 // smem: two stages of B (64 KB), wX (32 KB) and a chunk of x rows (16 KB) per pipeline, control.
 constexpr uint32_t kSegW = 8 * kTileB, kSegCtl = kSegW + 6 * kTileB;
 constexpr uint32_t kSegSmem = kSegCtl + 3072;
@@ -956,9 +956,9 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(const __grid_constant__
 // until the conv of the next has read them.
 // TMEM, per pipeline: what the chunk adds to S^T (64 columns), C S^T and P X (128), P (64).  S^T
 // itself stays in registers (32 of a row per thread): fp32 sums there round to nearest.
-// Bound by the chain of a chunk's phases (conv, scales, weights, products, epilogue): 8 to 9 us for
-// one pipeline alone, 10.8 for the two, with 39 % of issue slots and 9 % of the tensor pipe busy.
-// 4096 tokens of 32 heads of 128 102 us, 65,536 of 64 heads of 64 1213 us, 40,677 in eight 926 us.
+// Bound by the chain of a chunk's phases (conv, scales, weights, products, epilogue): 9 us for the
+// two pipelines, with 45 % of issue slots and 11 % of the tensor pipe busy.
+// 4096 tokens of 32 heads of 128 95 us, 65,536 of 64 heads of 64 1012 us, 40,677 in eight 809 us.
 constexpr uint32_t kMainPipe = 6 * kTileB, kMainCtl = kMainPipe + 8 * kTileB;
 constexpr uint32_t kMainSmem = kMainCtl + 3072;
 

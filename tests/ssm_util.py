@@ -84,6 +84,7 @@ def layer(i, H, G, P, N, dt_min=0.0, dt_max=np.inf, S0=None):
 #: them in two parts too: 2 2^-14.  bf16 activations round each to 11 bits once, 2^-11: two factors
 #: are 2^-10, plus the state's 2^-14 and the scores' 2^-14; then one rounding of the result to bf16,
 #: 2^-8 of it.
+#: (Factors in two fp16 parts, 11 bits each, leave less: the bounds hold for both.)
 #: The silu of a conv sum a = sum of terms with magnitude m is off by at most 1.1 eps m; relative to
 #: its value that is unbounded near a zero of the sum, so a factor counts with at least 2^-6 m:
 #: 2^-24 4 m (the fp32 sum) over 2^-6 m is 2^-16.
