@@ -1078,8 +1078,11 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
   for (int q = 0; q < 32; ++q) smax = fmaxf(smax, fabsf(sv[q]));
   if (s.live) {
     uint32_t halo[3];
-    const Taps taps = load_taps2(a, s, lane);
-    if (nch > 0) load_x(g, un, s, un.s + c0 * kL, warp, lane, S16, halo);
+    Taps taps{};
+    if (nch > 0) {  // (a call without a token may have neither taps nor rows)
+      taps = load_taps2(a, s, lane);
+      load_x(g, un, s, un.s + c0 * kL, warp, lane, S16, halo);
+    }
     for (int k = 0; k < nch; ++k) {
       const int t0 = un.s + (c0 + k) * kL, L = min(kL, un.e - t0);
       const size_t chunk = (size_t)(un.chunk + c0 + k), at = chunk * a.G + grp;
