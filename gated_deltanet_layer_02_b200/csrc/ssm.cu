@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) ssm_scan_kernel(SsmArgs a) {
                     ? __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(a.S0) + sbase +
                                                              (size_t)(4 * q) * NS + 32 * m))
                     : make_float4(0.f, 0.f, 0.f, 0.f);
-  const float rate = -expf(a.a_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  const float rate = -ssm_rate(a.a_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   const float D = a.D ? a.D[h] : 0.f;
   const int cB = a.H * a.P + (h / (a.H / a.G)) * NS, cC = cB + a.G * NS;
   const int cx = h * a.P + pb * kRows;
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) ssm_step_kernel(SsmArgs a, in
     const int h = g * per + (b0 + b) / blocks;
     const float d = ssm_step(a.dt[(size_t)n * a.H + h] + (a.dt_bias ? a.dt_bias[h] : 0.f), a.dt_min,
                              a.dt_max);
-    gate_s[b] = make_float2(expf(-expf(a.a_log[h]) * d), d);
+    gate_s[b] = make_float2(expf(-ssm_rate(a.a_log[h]) * d), d);
   }
   // ---- conv + SiLU, 4 channels per item: B, C, then this CTA's x
   const int cB = a.H * a.P + g * NS;

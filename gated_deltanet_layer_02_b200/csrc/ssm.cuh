@@ -24,6 +24,13 @@ __device__ __forceinline__ float ssm_step(float v, float lo, float hi) {
   return sp < lo ? lo : (sp > hi ? hi : sp);
 }
 
+// exp(a_log), held at 2.3e38 (finite in log2 too): past it a token with a step forgets all before
+// it, and one without a step nothing (0 times an infinity would be NaN).  A NaN stays one.
+__device__ __forceinline__ float ssm_rate(float a_log) {
+  const float r = expf(a_log);
+  return r > 2.3e38f ? 2.3e38f : r;
+}
+
 template <typename T>
 __device__ __forceinline__ void load8_or_zero(const T* p, float (&v)[8]) {
   if (p) {

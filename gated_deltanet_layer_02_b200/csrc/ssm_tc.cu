@@ -377,7 +377,7 @@ __device__ __forceinline__ void gates(const SsmTcArgs& g, const Unit& un, int pa
   for (int hh = warp; hh < kGateHeads; hh += 16) {
     const int h = h0 + hh;
     if (h >= a.H) break;
-    const float rate2 = -1.4426950408889634f * expf(a.a_log[h]);
+    const float rate2 = -1.4426950408889634f * ssm_rate(a.a_log[h]);
     const float4 d4 = *reinterpret_cast<const float4*>(d_s + hh * 132 + 4 * lane);
     const float d[4] = {d4.x, d4.y, d4.z, d4.w};
     double c[4], sum = 0.0;

@@ -7,7 +7,9 @@ import pytest
 import torch
 
 import gated_deltanet_layer_02_b200 as gdn
-from gpu_util import ensure_built
+import ssm_util as U
+from gpu_util import dev, ensure_built
+from test_gpu_ssm import prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +37,34 @@ def test_sequences_without_a_token_need_no_rows(dtype, N):
     torch.cuda.synchronize()
     assert rc == gdn.GDN_OK and int(status.item()) == 0
     assert torch.equal(SN, S0) and torch.equal(convN, conv0)
+
+
+@DTYPES
+@pytest.mark.parametrize("lens", [(127,), (128,), (130, 5)], ids=str)
+def test_rate_past_fp32(lens, dtype):
+    # exp(a_log) overflows: a token with a step forgets everything before it, one without a step
+    # (softplus underflows) forgets nothing, and what lies behind the last token plays no part
+    shape = (4, 2, 64, 128)
+    i = U.inputs(*shape, lens, dtype, seed=50)
+    i["a_log"][1] = 90.0
+    i["dt"][3:9, 1] = -200.0
+    i["dt"][lens[0] - 1, 1] = -200.0
+    U.check_layer(prefill(i, gdn.SsmDims(*shape)), U.layer(i, *shape), dtype, f"rate {lens}")
+
+
+@DTYPES
+def test_rate_past_fp32_of_one_token(dtype):
+    shape, B = (4, 2, 64, 128), 3
+    dims = gdn.SsmDims(*shape)
+    i = U.inputs(*shape, (1,) * B, dtype, seed=51)
+    i["a_log"][1] = 90.0
+    i["dt"][1, 1] = -200.0
+    ref = U.layer(i, *shape)
+    ensure_built()
+    S, c = dev(i["S0"]), dev(i["conv0"])
+    o = gdn.ssm_decode_step(dev(i["x"]), dev(i["dt"]), dev(i["a_log"]), c, S, dev(i["conv_w"]),
+                            conv_b=dev(i["conv_b"]), dt_bias=dev(i["dt_bias"]), D=dev(i["D"]),
+                            z=dev(i["z"]), dims=dims)
+    torch.cuda.synchronize()
+    U.check(o, ref[0], ref[3], U.OUT_F32, "out", 2.0 ** -8 if dtype == BF else 0.0)
+    U.check(S, ref[1], ref[4], U.STATE, "state")
