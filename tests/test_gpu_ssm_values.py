@@ -68,3 +68,33 @@ def test_rate_past_fp32_of_one_token(dtype):
     torch.cuda.synchronize()
     U.check(o, ref[0], ref[3], U.OUT_F32, "out", 2.0 ** -8 if dtype == BF else 0.0)
     U.check(S, ref[1], ref[4], U.STATE, "state")
+
+
+@DTYPES
+def test_gate_far_below_zero(dtype):
+    # silu(z) = z / (1 + exp(-z)) keeps its relative precision down to where it underflows, and is
+    # zero below
+    shape = (4, 2, 64, 128)
+    i = U.inputs(*shape, (70, 9), dtype, seed=52)
+    values = [-30.0, -43.5, -50.0, -60.0, -88.0, -100.0, -1e10, -1e30, torch.finfo(BF).min]
+    z = i["z"].view(-1)
+    for k, v in enumerate(values):
+        z[k::16] = v
+    U.check_layer(prefill(i, gdn.SsmDims(*shape)), U.layer(i, *shape), dtype, "gate")
+
+
+@pytest.mark.parametrize("what", ["x", "B", "C"])
+def test_conv_output_far_below_zero(what):
+    # silu is zero at -200 and below: the same bits whatever the value
+    shape = (4, 2, 64, 128)
+    dims = gdn.SsmDims(*shape)
+    i = U.inputs(*shape, (150,), BF, seed=53, init=False)
+    c = {"x": 70, "B": 4 * 64 + 5, "C": 4 * 64 + 2 * 128 + 5}[what]
+    i["conv_w"][c] = torch.tensor([0.0, 0.0, 0.0, 1.0])
+    got = []
+    for v in (-200.0, -1e30):
+        i["x"][17, c] = i["x"][131, c] = v
+        got.append(prefill(i, dims))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    U.check_layer((got[1][0], None, None), U.layer(dict(i, x=i["x"].clamp(min=-200.0)), *shape), BF,
+                  what)
