@@ -989,7 +989,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
   uint32_t* top_s = reinterpret_cast<uint32_t*>(mine);      // [8] largest magnitudes of S
   float* m_s = reinterpret_cast<float*>(mine + 64);         // [4] maxima of g of the blocks
   float* pm_s = reinterpret_cast<float*>(mine + 128);       // [128] running maximum of g
-  __half* f_s = reinterpret_cast<__half*>(pm_s + kL);       // [128] F: 2^(g - maximum of the block)
+  float* f_s = pm_s + kL;                                   // [128] F: 2^(g - maximum of the block)
   int8_t* ex_s = reinterpret_cast<int8_t*>(f_s + kL);       // [128] exponents of the rows of X
   if (tid == 0) {
     for (int k = 0; k < 4; ++k) mbar_init(c_full + k, 1);
@@ -1186,7 +1186,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
         if (quad == 2) pm = fmaxf(pm, M1 + bt.y);
         if (quad == 3) pm = fmaxf(pm, M2 + bt.z);
         pm_s[i] = pm;
-        f_s[i] = __float2half_rn(ex2(gi - (quad == 0 ? M0 : (quad == 1 ? M1 : (quad == 2 ? M2 : M3)))));
+        f_s[i] = ex2(gi - (quad == 0 ? M0 : (quad == 1 ? M1 : (quad == 2 ? M2 : M3))));
         if (pt == 0) *reinterpret_cast<float4*>(m_s) = make_float4(M0, M1, M2, M3);
       }
       // C B^T of this thread's columns: 16 of each block of 32 up to the diagonal
@@ -1214,8 +1214,9 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
         }
         __syncwarp();
       }
-      // ---- P^ (fp16) into TMEM.  ref: the blocks' maxima from this block's start on; cs: decay up
-      // to this block
+      // ---- P^ (fp16) into TMEM, its weights in fp32: one token with a large channel makes those of
+      // the others small for all channels.  ref: the blocks' maxima from this block's start on; cs:
+      // decay up to this block
       const float pm = pm_s[i];
       float cs = 0.f;
       {
@@ -1240,17 +1241,13 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
             uint32_t out[8];
             const int j0 = blk * 32 + half * 16;
             if (blk < quad) {
-              const __half2 rf = __float2half2_rn(ex2(ref[blk < 3 ? blk : 2] - pm));
+              const float rf = ex2(ref[blk < 3 ? blk : 2] - pm);
 #pragma unroll
-              for (int p = 0; p < 2; ++p) {
-                const uint4 fr = *reinterpret_cast<const uint4*>(f_s + j0 + 8 * p);
-                const uint32_t f[4] = {fr.x, fr.y, fr.z, fr.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&in[4 * p + q]),
-                                            __hmul2(*reinterpret_cast<const __half2*>(&f[q]), rf));
-                  out[4 * p + q] = *reinterpret_cast<const uint32_t*>(&v);
-                }
+              for (int q = 0; q < 8; q += 2) {
+                const float4 f = *reinterpret_cast<const float4*>(f_s + j0 + 2 * q);
+                out[q] = pack_f16x2(__fmul2_rn(unpack_f16x2(in[q]), mul2(make_float2(f.x, f.y), rf)));
+                out[q + 1] =
+                    pack_f16x2(__fmul2_rn(unpack_f16x2(in[q + 1]), mul2(make_float2(f.z, f.w), rf)));
               }
             } else {
               // the diagonal block: g of its tokens is in the lanes of this warp

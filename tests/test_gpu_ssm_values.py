@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import gated_deltanet_layer_02_b200 as gdn
+import ssm_bounds as SB
 import ssm_util as U
 from gpu_util import dev, ensure_built
 from test_gpu_ssm import prefill
@@ -98,3 +99,35 @@ def test_conv_output_far_below_zero(what):
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
     U.check_layer((got[1][0], None, None), U.layer(dict(i, x=i["x"].clamp(min=-200.0)), *shape), BF,
                   what)
+
+
+def one_large(mag, L, what="x", seed=40):
+    """A prompt with slow decays, in which token 10 has one value of about `mag` among ones."""
+    i = U.inputs(2, 1, 64, 128, (L,), BF, seed, init=False, gate=False, direct=False)
+    i["a_log"].fill_(-3.0)
+    c = 5 if what == "x" else 2 * 64 + 7
+    i["conv_w"][c] = torch.tensor([0.0, 0.0, 0.0, 1.0])
+    i["x"][10, c] = mag
+    if what == "B":  # where C is zero: no output shows the value itself
+        i["conv_w"][c + 128], i["conv_b"][c + 128] = 0.0, 0.0
+    return i
+
+
+@pytest.mark.parametrize("L", [128, 300])
+@pytest.mark.parametrize("what", ["x", "B"])
+@pytest.mark.parametrize("e", [19, 20, 22])
+def test_one_large_value_leaves_the_others(e, what, L):
+    # 2^22 times as large as the others of its row: they keep the ordinary bound
+    i = one_large(2.0 ** e, L, what)
+    U.check_layer(prefill(i, gdn.SsmDims(2, 1, 64, 128)), U.layer(i, 2, 1, 64, 128), BF,
+                  f"{what} 2^{e}")
+
+
+@pytest.mark.parametrize("what", ["x", "B"])
+@pytest.mark.parametrize("e", [0, 24, 30])
+def test_one_large_value_within_the_bound_of_fp16_operands(e, what):
+    i = one_large(2.0 ** e, 128, what, seed=41)
+    o, S, _ = prefill(i, gdn.SsmDims(2, 1, 64, 128))
+    out, SN, b_out, b_SN = SB.chunk_bounds(i, 2, 1, 64, 128)
+    assert SB.worst(o, out, b_out) <= 1.0
+    assert SB.worst(S, SN, b_SN) <= 1.0
