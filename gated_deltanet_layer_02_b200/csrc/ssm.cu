@@ -20,26 +20,43 @@ constexpr int kScanThreads = 128;
 constexpr int kScanRows = 64;   // rows of the state per CTA (16 per warp, 8 lanes per row)
 constexpr int kConvRun = 4;    // tokens per thread of the packed conv
 
+// The sequence that holds token t, for a whole block (-1: none).  In a table without bad entries a
+// binary search finds it.  Where that finds none (rows behind the last sequence; entries out of
+// order) the block's threads look at every sequence: a bad entry costs no other sequence its rows.
+__device__ __forceinline__ int block_seq_of_token(const SsmArgs& a, int t, int& s, int& end) {
+  __shared__ int found;
+  const int n = seq_of_token(a.cu, a.N, t);
+  s = __ldg(a.cu + n), end = __ldg(a.cu + n + 1);
+  if (s >= 0 && s <= t && t < end && end <= a.T) return n;
+  __syncthreads();
+  if (threadIdx.x == 0) found = -1;
+  __syncthreads();
+  for (int m = threadIdx.x; m < a.N; m += blockDim.x) {
+    const int ms = __ldg(a.cu + m), me = __ldg(a.cu + m + 1);
+    if (ms >= 0 && ms <= t && t < me && me <= a.T) atomicMax(&found, m);
+  }
+  __syncthreads();
+  const int m = found;
+  if (m >= 0) s = __ldg(a.cu + m), end = __ldg(a.cu + m + 1);
+  return m;
+}
+
 // Packed prompts: a thread owns 8 channels and a run of kConvRun tokens, the three rows before
 // the current one in registers.
 __global__ void __launch_bounds__(128) ssm_conv_kernel(SsmArgs a) {
   const int c = (blockIdx.y * 128 + threadIdx.x) * 8, t0 = blockIdx.x * kConvRun;
-  if (c >= a.Cc) return;
+  const bool live = c < a.Cc;
   float w[4][8], b[8];
-  load_taps<float>(a, c, w, b);
+  if (live) load_taps<float>(a, c, w, b);
   const float* x = static_cast<const float*>(a.x) + c;
   const float* c0 = static_cast<const float*>(a.conv0);
   float h[3][8];
-  int n = seq_of_token(a.cu, a.N, t0) - 1, s = 0, end = 0;
+  int n = -1, s = 0, end = 0;
   const int t1 = min(a.T, t0 + kConvRun);
-  bool fresh = true;  // the history registers do not hold the rows before t
   for (int t = t0; t < t1; ++t) {
-    while (n < a.N && t >= end) {  // the next sequence that may hold t
-      ++n;
-      if (n < a.N) seq_range(a, n, s, end);
-      fresh = true;
-    }
-    if (n >= a.N || t < s) continue;  // behind the last sequence
+    const bool fresh = n < 0 || t >= end;  // the history registers do not hold the rows before t
+    if (fresh) n = block_seq_of_token(a, t, s, end);
+    if (n < 0 || !live) continue;
     if (fresh) {
       const int row = state_row(a.slot, n, a.num_slots);
 #pragma unroll
@@ -50,7 +67,6 @@ __global__ void __launch_bounds__(128) ssm_conv_kernel(SsmArgs a) {
                                                : nullptr),
                       h[j]);
       }
-      fresh = false;
     }
     float v[8], out[8];
     load8(x + (size_t)t * a.Cc, v);

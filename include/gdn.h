@@ -341,7 +341,9 @@ int gdn_decode_step_bf16_state(const gdn_dims* dims, gdn_dtype dtype, const void
  * call without z.  Rules of the file header apply; in addition every index that comes from
  * device memory (cu_seqlens, slot_idx) is checked on the device in every build: a sequence whose
  * cu_seqlens entries are out of order or past num_tokens counts as empty and sets dev_status to
- * GDN_ERR_INVALID_ARG.  Rows of `out` at and behind cu[N] are left as they were.
+ * GDN_ERR_INVALID_ARG; the others are computed, unless such entries make them overlap (no defined
+ * results then, but no access outside the tensors).  Rows of `out` that belong to no sequence (at
+ * and behind cu[N]) are left as they were.
  * Precision: fp32 sums and states throughout.  Prompts in bf16 go chunk by chunk (128 tokens)
  * through fp16 operands with power-of-two row scales: outputs are within 2^-10 + 2^-13 of the sum
  * of the magnitudes of what forms them (and rounded to bf16), the fp32 state within 2^-14 of it.

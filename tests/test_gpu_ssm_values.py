@@ -131,3 +131,34 @@ def test_one_large_value_within_the_bound_of_fp16_operands(e, what):
     out, SN, b_out, b_SN = SB.chunk_bounds(i, 2, 1, 64, 128)
     assert SB.worst(o, out, b_out) <= 1.0
     assert SB.worst(S, SN, b_SN) <= 1.0
+
+
+@DTYPES
+@pytest.mark.parametrize("cu", [(101, 203, 0, 101), (0, 50, -1, 101, 203, 203),
+                                (0, 50, 50, 2 ** 31 - 1, 50, 203)], ids=str)
+def test_bad_entries_cost_no_other_sequence_its_rows(cu, dtype):
+    # entries out of order or outside the rows: their sequences count as empty, the others are
+    # computed like any other
+    shape, T, N = (2, 1, 64, 128), 203, len(cu) - 1
+    good = [n for n in range(N) if 0 <= cu[n] <= cu[n + 1] <= T]
+    dims = gdn.SsmDims(*shape)
+    i = U.inputs(*shape, (T,), dtype, seed=55, init=False)
+    S0 = 0.1 * torch.randn(N, 2, 64, 128, generator=torch.Generator().manual_seed(4))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ensure_built()
+    ws = torch.full((gdn.ssm_prefill_workspace_size(N, T, dtype, dims),), 0x7f, dtype=torch.uint8,
+                    device="cuda")
+    o, S, c = gdn.ssm_prefill(
+        dev(i["x"]), dev(i["dt"]), dev(i["a_log"]), torch.tensor(cu, dtype=torch.int32).cuda(),
+        dev(i["conv_w"]), conv_b=dev(i["conv_b"]), dt_bias=dev(i["dt_bias"]), D=dev(i["D"]),
+        z=dev(i["z"]), S0=dev(S0), dims=dims, dev_status=status, workspace=ws)
+    torch.cuda.synchronize()
+    assert int(status.item()) == gdn.GDN_ERR_INVALID_ARG
+    for n in range(N):
+        if n not in good:
+            assert torch.equal(S[n].cpu(), S0[n])
+            continue
+        rows = slice(cu[n], cu[n + 1])
+        j = dict(i, x=i["x"][rows], dt=i["dt"][rows], z=i["z"][rows], S0=S0[n:n + 1],
+                 cu=torch.tensor([0, cu[n + 1] - cu[n]]))
+        U.check_layer((o[rows], S[n:n + 1], c[n:n + 1]), U.layer(j, *shape), dtype, f"sequence {n}")
