@@ -607,6 +607,8 @@ int ssm_prefill_impl(const gdn_ssm_dims* dims, gdn_dtype dtype, const void* x, c
   const void* ptrs[] = {x, conv_w, conv_b, dt, dt_bias, a_log, D, z, S0, SN, conv0, convN, out};
   for (const void* p : ptrs)
     if (p && misaligned(p)) return GDN_ERR_INVALID_ARG;
+  if (misaligned(cu, 4) || misaligned(slot, 4) || misaligned(dev_status, 4))
+    return GDN_ERR_INVALID_ARG;
   if (workspace && misaligned(workspace, 256)) return GDN_ERR_INVALID_ARG;
   // a grid covers every (sequence or chunk, head, 64 rows), or (chunk, group, gates of 32 heads)
   if (((int64_t)N + T / 128) * dims->num_heads * 2 > INT32_MAX)
@@ -698,6 +700,7 @@ int gdn_ssm_decode_step(const gdn_ssm_dims* dims, gdn_dtype dtype, gdn_dtype sta
   const void* ptrs[] = {x, conv_w, conv_b, dt, dt_bias, a_log, D, z, conv_state, S, out};
   for (const void* p : ptrs)
     if (p && misaligned(p)) return GDN_ERR_INVALID_ARG;
+  if (misaligned(slot_idx, 4) || misaligned(dev_status, 4)) return GDN_ERR_INVALID_ARG;
   // the grid covers every (sequence, group, CTA of its cluster); a CTA holds its conv outputs
   if ((int64_t)batch * dims->num_groups * gdn_host::kStepCluster > INT32_MAX ||
       gdn_host::step_blocks(dims->num_heads, dims->num_groups, dims->head_dim) >
