@@ -337,8 +337,10 @@ int gdn_decode_step_bf16_state(const gdn_dims* dims, gdn_dtype dtype, const void
  *   S_t   = exp(-exp(a_log[h]) delta) S_{t-1} + delta x_t B_t^T
  *   y_t   = S_t C_t + D[h] x_t
  *   out_t = y_t silu(z_t)                                             (when z is given)
- * The RMSNorm of a layer that has one is a call of its own: gdn_gated_rmsnorm on the rows of a
- * call without z.  Rules of the file header apply; in addition every index that comes from
+ * A norm is a call of its own.  gdn_gated_rmsnorm is the one for a layer that normalises first and
+ * then gates, norm(y) silu(z), over at most 1024 channels: on rows of a call without z.  It does not
+ * serve a layer that gates first, norm(y silu(z)): that one passes z here, and this library has no
+ * norm for what comes out.  Rules of the file header apply; in addition every index that comes from
  * device memory (cu_seqlens, slot_idx) is checked on the device in every build: a sequence whose
  * cu_seqlens entries are out of order or past num_tokens counts as empty and sets dev_status to
  * GDN_ERR_INVALID_ARG; the others are computed, unless such entries make them overlap (no defined
