@@ -102,28 +102,4 @@ struct PrefillArgs {
   float* carry_out;
 };
 
-// Selective state space layer: packed prefill, and one token per sequence (N = T).
-struct SsmArgs {
-  const void* x;         // [T][Cc] pre-conv rows [x | B | C]
-  const void* conv_w;    // [Cc][4]
-  const void* conv_b;    // [Cc] or NULL
-  const float* dt;       // [T][H]
-  const float* dt_bias;  // [H] or NULL
-  const float* a_log;    // [H]
-  const float* D;        // [H] or NULL
-  const void* z;         // [T][H][P] or NULL
-  const int32_t* cu;     // [N+1] (prompts)
-  const void* S0;        // initial states, or NULL
-  void* SN;              // final states, or NULL (may be S0)
-  const void* conv0;
-  void* convN;
-  void* out;
-  const int32_t* slot;   // [N] state-pool rows, or NULL (= n)
-  int32_t* status;
-  float* u;              // workspace: [T][Cc] conv outputs, fp32
-  int num_slots;
-  int N, T, H, G, P, Cc;
-  float dt_min, dt_max;
-};
-
 }  // namespace gdn

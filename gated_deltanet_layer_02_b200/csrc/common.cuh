@@ -61,12 +61,6 @@ __device__ __forceinline__ void load32(const void* p, uint4& lo, uint4& hi) {
                : "l"(p)
                : "memory");
 }
-// 32 bytes in one store (p 32-byte aligned).
-__device__ __forceinline__ void store32(void* p, const uint4& lo, const uint4& hi) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(lo.x), "r"(lo.y),
-               "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
-               : "memory");
-}
 // 16 values as bf16 (round to nearest even) in one 32-byte store: a whole L2 sector per lane
 // (p 32-byte aligned).
 __device__ __forceinline__ void store16(__nv_bfloat16* p, const float* v) {

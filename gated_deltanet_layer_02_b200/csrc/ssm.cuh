@@ -7,6 +7,37 @@
 
 namespace gdn {
 
+// Selective state space layer: packed prefill, and one token per sequence (N = T).
+struct SsmArgs {
+  const void* x;         // [T][Cc] pre-conv rows [x | B | C]
+  const void* conv_w;    // [Cc][4]
+  const void* conv_b;    // [Cc] or NULL
+  const float* dt;       // [T][H]
+  const float* dt_bias;  // [H] or NULL
+  const float* a_log;    // [H]
+  const float* D;        // [H] or NULL
+  const void* z;         // [T][H][P] or NULL
+  const int32_t* cu;     // [N+1] (prompts)
+  const void* S0;        // initial states, or NULL
+  void* SN;              // final states, or NULL (may be S0)
+  const void* conv0;
+  void* convN;
+  void* out;
+  const int32_t* slot;   // [N] state-pool rows, or NULL (= n)
+  int32_t* status;
+  float* u;              // workspace: [T][Cc] conv outputs, fp32
+  int num_slots;
+  int N, T, H, G, P, Cc;
+  float dt_min, dt_max;
+};
+
+// 32 bytes in one store (p 32-byte aligned).
+__device__ __forceinline__ void store32(void* p, const uint4& lo, const uint4& hi) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(lo.x), "r"(lo.y),
+               "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+               : "memory");
+}
+
 // Tokens [s, e) of sequence n.  Entries of cu that are out of order or past T give an empty range
 // and GDN_ERR_INVALID_ARG.
 __device__ __forceinline__ void seq_range(const SsmArgs& a, int n, int& s, int& e) {
