@@ -5,11 +5,14 @@
 //   Y    = diag(2^cum) C S^T + P X,   P_ij = 2^(cum_i - cum_j) delta_j C_i.B_j  (j <= i)
 //   S^T <- 2^cum_L S^T + B^T diag(w) X,   w_j = 2^(cum_L - cum_j) delta_j
 // Precision.  All products take fp16 operands (11 bits) and sum in fp32.  Outputs are rounded to
-// bf16, so their operands are rounded to fp16 once.  The state is returned in fp32, so its update
-// keeps both factors in two fp16 parts (three products; what is left out is 2^-22 of them).  fp16
-// has few exponent bits: rows of C, B and X are scaled by a power of two each (exponent from the
-// row's largest value), S and wX by one per chunk, and P by the row's largest weight.  Nothing
-// overflows then, and what underflows is 2^-24 of what it is added to.  With the exponents eX, eB of
+// bf16, so what forms them is rounded to fp16 wherever it becomes an operand or is stored: C, B, C B^T,
+// P, X for P X, C and S for C S^T, X for D X.  The state is returned in fp32, so its update keeps both
+// factors in two fp16 parts (three products; what is left out is 2^-22 of them).  fp16 has few exponent
+// bits: rows of C, B and X are scaled by a power of two each (exponent from the row's largest value), S
+// and wX by one per chunk, and P by the row's largest weight.  Nothing overflows then.  What underflows
+// is small beside the largest value of its scale: 2^-28 of it for C, 2^-38 for B and X, 2^-30 for a
+// token's share of P X beside the largest token's (fp32 weights; the sums of gdn.h).  It may still be
+// all that a channel has: 64 channels of X share a scale.  With the exponents eX, eB of
 // rows of X and B: g_j = log2(delta_j) - cum_j + eX_j + eB_j, pm_i = max over j <= i of g_j,
 //   P^_ij = (C^_i.B^_j) 2^(g_j - pm_i)
 // (never above the product), and row i of the result counts 2^(cum_i + pm_i + exponent of C_i).

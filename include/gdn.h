@@ -347,11 +347,19 @@ int gdn_decode_step_bf16_state(const gdn_dims* dims, gdn_dtype dtype, const void
  * results then, but no access outside the tensors).  Rows of `out` that belong to no sequence (at
  * and behind cu[N]) are left as they were.
  * Precision: fp32 sums and states throughout.  Prompts in bf16 go chunk by chunk (128 tokens)
- * through fp16 operands with power-of-two row scales: outputs are within 2^-10 + 2^-13 of the sum
- * of the magnitudes of what forms them (and rounded to bf16), the fp32 state within 2^-14 of it.
+ * through fp16 operands with power-of-two scales: one for a token's row of B, of C and of 64 channels
+ * of x (of a head, from a multiple of 64 on), one for 64 rows of a state.  What forms an output is
+ * rounded to 11 bits up to five times (C, B, their product, that with its weight, x), so before it is
+ * rounded to bf16 the output is within 5 2^-11 + 2^-13 of the sum of the magnitudes of what forms it.
+ * The state's factors have 22 bits: it is within 2^-14 of that sum, most of it left to conv outputs
+ * whose terms cancel.  Values far smaller than the largest one that shares their scale have an
+ * absolute error instead, in parts of that largest value: 2^-28 for C, 2^-38 for B and x, 2^-39 for
+ * the state that enters, and 2^-30 (2^-36 in the state) for what a token brings beside the token of
+ * its chunk that brings most.  So x and B keep their 11 bits down to 2^-27 of the row's largest value.
  * NaN and infinity reach only outputs from their token on.  A NaN or infinity among the conv
  * outputs of x makes, in a bf16 prompt, the head's 64 channels around it NaN (channels 0-63 or
- * 64-127), and one in B all states of its group; single tokens and fp32 prompts follow the formula.
+ * 64-127), as does an infinity in an initial state, and one in B all states of its group; single
+ * tokens and fp32 prompts follow the formula.
  */
 typedef struct gdn_ssm_dims {
   int32_t num_heads;   /* H: a multiple of num_groups */

@@ -17,9 +17,13 @@ So a term of P x is rounded five times, one of C S twice, D x once.  The state's
 parts each, 2^-22 of the value; the second part too ends at 2^-25 of the scaled value:
   B     2^-38 B_j;   w x   2^14 > max >= 2^12 by the factors' exponents:  2^-36 |B_jn| / B_j max(w X B)
 fp32 arithmetic around it (conv, silu, gates, sums): 2^-13 for outputs and 2^-14 for states, as in
-ssm_util.  Where the conv is one tap of weight 1 (nothing cancels) and the decays are slow, that is
-less: silu 2^-21 per factor, weights 2^-20, two parts 3 2^-22, and fp32 sums of 3 products of 8
-steps, each step at most 2^-23 of what has been summed: 24 2^-23.  In all below 2^-17.
+ssm_util.  Where the conv is one tap of weight 1, so that nothing cancels, the values are below 8 and
+the decays slow, that is less (TIGHT_*).  A silu is off by 2^-20.5 (exp2 2 units of 2^-23 and up to
+2^-21 from its argument, reciprocal, sum and product one each), a weight by 2^-20, two parts leave
+3 2^-22 (each factor, and the product of the two second parts).  Products are summed 16 at a time; each
+addend counts as off by 2^-23 of the largest.  A state of at most 5 tokens is 3 such sums of 6 addends:
+2 2^-20.5 + 2^-20 + 3 2^-22 + 18 2^-23 < 2^-17.  An output has a third factor, and C.B and C S are 8 sums
+of 17: 3 2^-20.5 + 2^-20 + (136 + 6) 2^-23 < 2^-15.
 """
 import numpy as np
 
@@ -27,6 +31,7 @@ import ssm_util as U
 
 FIVE = 5.02 * 2.0 ** -11   # (1 + 2^-11)^5 - 1
 HALF_BF16 = 2.0 ** -8
+TIGHT_OUT, TIGHT_STATE = 2.0 ** -15, 2.0 ** -17
 
 
 def chunk_bounds(i, H, G, P, N, out_rel=2.0 ** -13, state_rel=2.0 ** -14):

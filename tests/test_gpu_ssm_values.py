@@ -162,3 +162,57 @@ def test_bad_entries_cost_no_other_sequence_its_rows(cu, dtype):
         j = dict(i, x=i["x"][rows], dt=i["dt"][rows], z=i["z"][rows], S0=S0[n:n + 1],
                  cu=torch.tensor([0, cu[n + 1] - cu[n]]))
         U.check_layer((o[rows], S[n:n + 1], c[n:n + 1]), U.layer(j, *shape), dtype, f"sequence {n}")
+
+
+def spread(shape, lens, seed, e=12):
+    """Inputs whose channels of x, B and C, and elements of the state, differ by up to 2^(2 e)."""
+    H, G, P, N = shape
+    i = U.inputs(*shape, lens, BF, seed=seed)
+    gen = torch.Generator().manual_seed(seed)
+    i["x"] = (i["x"].float() * 2.0 ** torch.randint(-e, e + 1, (1, H * P + 2 * G * N),
+                                                    generator=gen)).to(BF)
+    i["S0"] = i["S0"] * 2.0 ** torch.randint(-e, e + 1, (1, H, P, N), generator=gen)
+    i["conv0"], i["conv_b"] = None, None
+    return i
+
+
+@pytest.mark.parametrize("shape", [(4, 2, 64, 128), (2, 1, 128, 64)], ids=str)
+@pytest.mark.parametrize("lens", [(1,), (3,), (5, 0, 2), (40, 128)], ids=str)
+def test_channels_of_other_magnitudes(lens, shape):
+    # short sequences too, in which no errors average out
+    i = spread(shape, lens, seed=60 + len(lens))
+    o, S, _ = prefill(i, gdn.SsmDims(*shape))
+    out, SN, b_out, b_SN = SB.chunk_bounds(i, *shape)
+    assert SB.worst(o, out, b_out) <= 1.0
+    assert SB.worst(S, SN, b_SN) <= 1.0
+
+
+def exact_conv(shape, lens, seed):
+    """Inputs whose conv is its last tap alone, with slow decays."""
+    i = U.inputs(*shape, lens, BF, seed=seed, bias=False)
+    i["conv_w"] = torch.tensor([0.0, 0.0, 0.0, 1.0], dtype=BF).repeat(i["conv_w"].shape[0], 1)
+    i["conv0"] = None
+    i["x"] = i["x"].clamp(-7.0, 7.0)
+    i["a_log"].fill_(-6.0)
+    return i
+
+
+@pytest.mark.parametrize("shape", [(4, 2, 64, 128), (2, 1, 128, 64)], ids=str)
+@pytest.mark.parametrize("lens", [(1,), (2,), (5, 0, 3, 1)], ids=str)
+def test_both_parts_of_the_state_factors_count(lens, shape):
+    i = exact_conv(shape, lens, seed=70 + len(lens))
+    o, S, _ = prefill(i, gdn.SsmDims(*shape))
+    out, SN, b_out, b_SN = SB.chunk_bounds(i, *shape, SB.TIGHT_OUT, SB.TIGHT_STATE)
+    assert SB.worst(o, out, b_out) <= 1.0
+    assert SB.worst(S, SN, b_SN) <= 1.0
+
+
+def test_both_parts_count_in_a_state_that_segments_hand_on():
+    # three tokens at the start of a sequence of 16 chunks; the others bring nothing.  Each chunk's
+    # decay and the product with it are off by 2^-23 and 2^-24: with 16 of them below 2^-18 more
+    shape, T = (2, 1, 64, 128), 2000
+    i = exact_conv(shape, (T,), seed=75)
+    i["x"][3:] = 0
+    o, S, _ = prefill(i, gdn.SsmDims(*shape))
+    _, SN, _, _, scale = U.layer(i, *shape)
+    assert SB.worst(S, SN, (SB.TIGHT_STATE + 2.0 ** -18) * scale + 2.0 ** -100) <= 1.0
