@@ -49,7 +49,8 @@ EXPORTS = (
 STATIC_WORKSPACE_BYTES = 64 << 20
 
 
-GDN_FAULT_NONE, GDN_FAULT_SKIP_CHAIN_LOAD = 0, 1
+GDN_FAULT_NONE, GDN_FAULT_SKIP_CHAIN_LOAD, GDN_FAULT_SKIP_SSM_PRODUCT, \
+    GDN_FAULT_SKIP_SSM_SEG_LOAD, GDN_FAULT_SKIP_SSM_LOAD = range(5)
 
 
 class DebugOptions(ctypes.Structure):

@@ -507,7 +507,7 @@ int gdn_debug_set(const gdn_debug_options* opts) {
   const bool split_ok = opts->chain_split == 0 || opts->chain_split == 1 ||
                         opts->chain_split == 2 || opts->chain_split == 4;
   if (opts->wait_limit_us > 10000000u || opts->segment_chunks < 0 || !split_ok ||
-      (opts->fault != GDN_FAULT_NONE && opts->fault != GDN_FAULT_SKIP_CHAIN_LOAD) ||
+      opts->fault < GDN_FAULT_NONE || opts->fault > GDN_FAULT_SKIP_SSM_LOAD ||
       opts->fault_chunk < 0)
     return GDN_ERR_INVALID_ARG;
   gdn_host::t_debug = *opts;

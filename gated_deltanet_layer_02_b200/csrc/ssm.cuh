@@ -126,6 +126,8 @@ struct SsmTcArgs {
   double* seg_decay;     // [segments][H] log2 of its decay
   uint64_t wait_ns;
   int NS, seg;           // state width; chunks per segment
+  int skip_bc, skip_seg, skip_main;  // debug fault injection: the product (bc) or the tiles' copy that
+                                     // the first CTA leaves out, counted in its own, or -1
 };
 
 }  // namespace gdn

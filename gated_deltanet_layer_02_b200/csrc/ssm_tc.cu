@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  if (tid == 0) {
+  if (tid == 0 && (blockIdx.x != 0 || g.skip_bc != 0)) {
     const uint32_t sB = smem_u32(sm), sC = sB + 2 * kTileB;
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
@@ -814,6 +814,7 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(const __grid_constant__
   const int users = min(2, slices - 2 * pair);
   const int nch = c1 - c0;
   auto load_b = [&](int k) {  // k-th chunk from the end
+    if (k == g.skip_seg && blockIdx.x == 0) return;
     const size_t at = (size_t)(un.chunk + c1 - 1 - k) * a.G + grp;
     mbar_arrive_expect_tx(full + (k & 1), 4 * kTileB);
     bulk_load(sm + (k & 1) * 4 * kTileB, g.tiles + at * kBcBytes + 2 * kTileB, 4 * kTileB,
@@ -1030,6 +1031,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
   const size_t pitch = (size_t)a.H * a.P * g.NS, sbase = (size_t)(s.c + p0) * g.NS + i;
   pdl_wait();
   auto load_tiles = [&](int c) {
+    if (c - c0 == g.skip_main && blockIdx.x == 0) return;
     const uint8_t* src = g.tiles + ((size_t)(un.chunk + c) * a.G + grp) * kBcBytes;
     mbar_arrive_expect_tx(c_full, 2 * kTileB);
     bulk_load(sm, src, 2 * kTileB, c_full);
@@ -1506,6 +1508,12 @@ cudaError_t launch_ssm_tc(gdn::SsmTcArgs g, void* workspace, cudaStream_t s) {
   g.seg = (int)l.seg;
   g.wait_ns = debug_opts().wait_limit_us ? (uint64_t)debug_opts().wait_limit_us * 1000ull
                                          : gdn::kWaitLimitNs;
+  const auto skip = [](int fault) {
+    return debug_opts().fault == fault ? debug_opts().fault_chunk : -1;
+  };
+  g.skip_bc = skip(GDN_FAULT_SKIP_SSM_PRODUCT);
+  g.skip_seg = skip(GDN_FAULT_SKIP_SSM_SEG_LOAD);
+  g.skip_main = skip(GDN_FAULT_SKIP_SSM_LOAD);
   const unsigned pairs = a.G * (((a.H / a.G) * (a.P / 64) + 1) / 2);
   const unsigned roles = a.G + (a.H + gdn::kGateHeads - 1) / gdn::kGateHeads;
   cudaError_t e = launch_tc(false, gdn::ssm_bc_kernel, (unsigned)(a.T / gdn::kL + a.N) * roles, 512,

@@ -531,6 +531,11 @@ int gdn_trace_span(gdn_trace* trace, int32_t i, float* start_ms, float* end_ms);
  *                  the call's table, sequence by sequence), so its bounded wait for that tile
  *                  runs out.  Used to test the timeout path with no GPU fault: the call then
  *                  reports GDN_ERR_TIMEOUT in dev_status and its outputs are undefined.
+ *                  Likewise for the bf16 prompts of the state space layer, whose first CTA leaves
+ *                  out, GDN_FAULT_SKIP_SSM_PRODUCT: C B^T (fault_chunk 0: of its chunk);
+ *                  GDN_FAULT_SKIP_SSM_SEG_LOAD: in the kernel of the segments' states, and
+ *                  GDN_FAULT_SKIP_SSM_LOAD: in the kernel of the outputs, the copy of a chunk's
+ *                  operand tiles (fault_chunk: its place among that CTA's chunks).
  *   fault_chunk    see fault.
  *   timestamps     device pointer (uint64, 1024 entries) or NULL: the kernels of the bf16
  *                  prefill that support it record %globaltimer stamps of their phases there
@@ -539,6 +544,9 @@ int gdn_trace_span(gdn_trace* trace, int32_t i, float* start_ms, float* end_ms);
  */
 #define GDN_FAULT_NONE 0
 #define GDN_FAULT_SKIP_CHAIN_LOAD 1
+#define GDN_FAULT_SKIP_SSM_PRODUCT 2
+#define GDN_FAULT_SKIP_SSM_SEG_LOAD 3
+#define GDN_FAULT_SKIP_SSM_LOAD 4
 typedef struct gdn_debug_options {
   uint32_t wait_limit_us;
   int32_t segment_chunks;

@@ -29,3 +29,14 @@ def test_index_arrays_are_aligned_to_their_type(L, which, dtype):
     if which != "cu_seqlens":
         assert L.gdn_ssm_decode_step(DIMS, dtype, 0, A, A, None, A, None, A, None, None, A, A, slot,
                                      4, 2, A, status, None) == gdn.GDN_ERR_INVALID_ARG
+
+
+def test_debug_faults_of_the_prefill_are_known(L):
+    for fault, want in ((gdn.GDN_FAULT_SKIP_SSM_PRODUCT, gdn.GDN_OK),
+                        (gdn.GDN_FAULT_SKIP_SSM_SEG_LOAD, gdn.GDN_OK),
+                        (gdn.GDN_FAULT_SKIP_SSM_LOAD, gdn.GDN_OK),
+                        (gdn.GDN_FAULT_SKIP_SSM_LOAD + 1, gdn.GDN_ERR_INVALID_ARG),
+                        (-1, gdn.GDN_ERR_INVALID_ARG)):
+        opts = gdn.DebugOptions(5000, 0, 0, fault, 0)
+        assert L.gdn_debug_set(ctypes.byref(opts)) == want
+        assert L.gdn_debug_set(None) == gdn.GDN_OK
