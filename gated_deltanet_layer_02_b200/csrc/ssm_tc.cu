@@ -734,9 +734,10 @@ __device__ __forceinline__ void mma_px(uint32_t lead, uint32_t tX, uint32_t tP, 
     mma_ts(lead, tX, tP + kk * 8, B + ((kk * 2048) >> 4), idesc_f16(128, 64, false, true), kk != 0);
 }
 
-// Exponent of the largest value row i of wX may hold (w, and the rows of X and B).
+// Exponent of the largest value row i of wX may hold (w, and the rows of X and B).  A weight of zero
+// (a token masked by its step) counts for nothing, however large its rows.
 __device__ __forceinline__ int weight_exponent(float w, int eX, int eB) {
-  return (int)(abs_bits(w) >> 23) - 127 + eX + eB;
+  return w == 0.f ? -1000 : (int)(abs_bits(w) >> 23) - 127 + eX + eB;
 }
 
 // The chunk's exponent of wX, by a whole warp (lane l: tokens 4 l .. 4 l + 3; every warp of the

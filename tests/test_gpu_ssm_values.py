@@ -216,3 +216,15 @@ def test_both_parts_count_in_a_state_that_segments_hand_on():
     o, S, _ = prefill(i, gdn.SsmDims(*shape))
     _, SN, _, _, scale = U.layer(i, *shape)
     assert SB.worst(S, SN, (SB.TIGHT_STATE + 2.0 ** -18) * scale + 2.0 ** -100) <= 1.0
+
+
+@pytest.mark.parametrize("lens", [(100,), (128, 40), (700,)], ids=str)
+@DTYPES
+def test_tokens_without_a_step_leave_the_state_whatever_their_rows_hold(dtype, lens):
+    # a padded batch that masks its last tokens by their steps: 0 times a row of 1e30 is nothing
+    shape, pad = (4, 2, 64, 128), 20
+    i = U.inputs(*shape, lens, dtype, seed=57)
+    for e in i["cu"][1:].tolist():
+        i["dt"][e - pad:e] = -1e4
+        i["x"][e - pad:e] *= 1e30
+    U.check_layer(prefill(i, gdn.SsmDims(*shape)), U.layer(i, *shape), dtype, "masked")
