@@ -221,7 +221,7 @@ constexpr int kTargetW = 12;   // wX below 2^14 (two factors, each below 2 of it
 // sequence.  A sequence without tokens has no chunk (kChunks) but one segment (kSegments: its state
 // is written too); kFollowed numbers the segments that another one follows, one fewer than a
 // sequence's segments, so that a batch of short sequences starts no CTA for them (96 sequences, 24
-// heads of 64: a call 169 -> 148 us).  Every warp finds its unit by itself, 128
+// heads of 64: a call 169 -> 148 us when it came in).  Every warp finds its unit by itself, 128
 // sequences at a time (4 per lane).  `most_units`: units the launch has room for.
 enum UnitKind { kChunks, kSegments, kFollowed };
 struct Unit {
@@ -349,8 +349,8 @@ __device__ __forceinline__ int cb_off(int blk, int half) { return (blk * 2 + hal
 // ------------------------------------------------------------------------------------- bc
 // 512 threads: warp w has tokens 8 w .. 8 w + 7 of the chunk, first of B, then of C; a lane holds 4
 // channels of a row.  State widths below 128 are padded with zero channels.
-// Bound by instructions: 63 % of issue slots, 1.5 TB/s.  4096 tokens of 16 groups 36 us, 65,536 of
-// 8 groups 229 us; one chunk 14 to 17 us, of which an empty launch is 6.
+// Bound by instructions: 63 % of issue slots, 1.5 TB/s.  4096 tokens of 16 groups 33 us, 65,536 of
+// 8 groups 230 us; one chunk 14 us, of which an empty launch is 6.
 constexpr uint32_t kBcSmem = 4 * kTileB + 2048;
 constexpr int kGateHeads = 32;  // heads per gates CTA
 
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(512, 2) ssm_bc_kernel(const __grid_constant__ 
   for (int part = 0; part < 2; ++part) {  // B, then C
     const int c = a.H * a.P + (part * a.G + grp) * g.NS + lane * 4;
     uint2 raw[11];  // the warp's rows and the three before them
-    if (inside) {  // all of the sequence: no checks per row (65,536 tokens: 250 us with them, 232 without)
+    if (inside) {  // all of the sequence: no checks per row (65,536 tokens: 248 us with them, 228 without)
       const __nv_bfloat16* r =
           static_cast<const __nv_bfloat16*>(a.x) + (size_t)(t0 + i0 - 3) * a.Cc + c;
 #pragma unroll
@@ -772,7 +772,7 @@ __device__ __forceinline__ void store_parts(float2 u, float w, uint8_t* W, uint3
 // The state a segment adds, the sum over its tokens of 2^(log decay from the token to the
 // segment's end) delta x B^T (for the first segment: and the decayed initial state), chunk by
 // chunk from its end; the chunks' contributions are added in fp32 registers.
-// 3.3 us per chunk of 128 channels; 65,536 tokens of 64 heads of 64 385 us, 55 % of issue slots busy.
+// 3.7 us per chunk of 128 channels; 65,536 tokens of 64 heads of 64 412 us, 52 % of issue slots busy.
 // smem: two stages of B (64 KB), wX (32 KB) and a chunk of x rows (16 KB) per pipeline, control.
 constexpr uint32_t kSegW = 8 * kTileB, kSegCtl = kSegW + 6 * kTileB;
 constexpr uint32_t kSegSmem = kSegCtl + 3072;
@@ -963,8 +963,8 @@ __global__ void __launch_bounds__(512, 1) ssm_seg_kernel(const __grid_constant__
 // TMEM, per pipeline: what the chunk adds to S^T (64 columns), C S^T and P X (128), P (64).  S^T
 // itself stays in registers (32 of a row per thread): fp32 sums there round to nearest.
 // Bound by the chain of a chunk's phases (conv, scales, weights, products, epilogue): 9 us for the
-// two pipelines, with 45 % of issue slots and 11 % of the tensor pipe busy.
-// 4096 tokens of 32 heads of 128 95 us, 65,536 of 64 heads of 64 1012 us, 40,677 in eight 809 us.
+// two pipelines, with 44 % of issue slots and 11 % of the tensor pipe busy.
+// 4096 tokens of 32 heads of 128 89 us, 65,536 of 64 heads of 64 1045 us, 40,677 in eight 791 us.
 constexpr uint32_t kMainPipe = 6 * kTileB, kMainCtl = kMainPipe + 8 * kTileB;
 constexpr uint32_t kMainSmem = kMainCtl + 3072;
 
@@ -1015,7 +1015,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
   if (row < 0 && tid == 0) report_status(a.status, GDN_ERR_INVALID_ARG);
   const float D = a.D ? a.D[s.h] : 0.f;
   // whole sectors of z and of the output, where their addresses allow it (40,677 tokens in eight
-  // sequences: 799 us; with z in 16-byte pieces 822)
+  // sequences: a call 837 us; with z in 16-byte pieces 848)
   const bool wide =
       ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.z)) & 31u) == 0;
   auto load_z = [&](const __nv_bfloat16* p, uint4& lo, uint4& hi) {
@@ -1345,7 +1345,7 @@ __global__ void __launch_bounds__(512, 1) ssm_main_kernel(const __grid_constant_
             if (a.z) y = __fmul2_rn(y, silu2(unpack_bf16x2(zw[e])));
             ow[e] = pack_bf16x2(y.x, y.y);
           }
-          // two quarters leave together (with 16-byte stores, in the case above, 868 us become 924)
+          // two quarters leave together (with 16-byte stores, in the case above, 837 us become 869)
           const uint4 now = make_uint4(ow[0], ow[1], ow[2], ow[3]);
           if ((r & 1) == 0) {
             even = now;
@@ -1399,12 +1399,13 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // One sequence: the length with the least time, counted in chunks of main: a CTA's chunks and half a
 // one to begin, whole segments over the SMs and then the shorter last ones, and 0.36 for a chunk of
 // the segments that seg goes over first.  Measured at 65,536 tokens of 64 heads: segments of 29
-// chunks 1719 us, of 37 1881 and of 64 1923 us, 1.09 and 1.12 times as long (the count says 1.11 and
-// 1.09); of 56, which it chooses, 1645 us.  4096 tokens of 32 heads of 128: 8 chunks 177 us, 4 242.
+// chunks 1694 us, of 37 1826 and of 64 1762 us, 1.08 and 1.04 times as long (the count says 1.11 and
+// 1.09); of 56, which it chooses, 1604 to 1689 us by the clocks.  4096 tokens of 32 heads of 128: 8
+// chunks, which it chooses, 147 us, 4 167, 16 248.
 // Several (whose lengths only the device knows): an SM's even share of the chunks, so that a sequence
 // is cut only if it alone would keep its SMs longer than the whole call should take; every other cut
 // costs a second conv and state update.  8 sequences of 20 to 56 chunks (bf16, 64 heads of 64): a
-// call took 1209 us with up to 4 waves and the units in order, and takes 966 us so.
+// call takes 837 us so, 959 in segments of 19 (four waves), and 885 with the units in order.
 constexpr int kSms = 148, kMostWaves = 4;
 // Until the last SM is through with n CTAs of `a` and then m of `b` <= a.
 double makespan(int64_t n, double a, int64_t m, double b) {
