@@ -228,3 +228,18 @@ def test_tokens_without_a_step_leave_the_state_whatever_their_rows_hold(dtype, l
         i["dt"][e - pad:e] = -1e4
         i["x"][e - pad:e] *= 1e30
     U.check_layer(prefill(i, gdn.SsmDims(*shape)), U.layer(i, *shape), dtype, "masked")
+
+
+@DTYPES
+@pytest.mark.parametrize("first", [1, 2, 150])
+def test_rows_before_the_first_sequence_stay(first, dtype):
+    shape, T = (2, 1, 64, 128), 290
+    i = U.inputs(*shape, (T - first,), dtype, seed=58)
+    want = prefill(i, gdn.SsmDims(*shape))
+    pad = lambda t: torch.cat([torch.full((first, *t.shape[1:]), float("nan"), dtype=t.dtype), t])  # noqa: E731
+    j = dict(i, x=pad(i["x"]), dt=pad(i["dt"]), z=pad(i["z"]), cu=i["cu"] + first)
+    out = torch.full((T, 2, 64), 7.0, dtype=dtype, device="cuda")
+    got = prefill(j, gdn.SsmDims(*shape), out=out)
+    assert torch.all(out[:first] == 7.0)
+    for a, b in zip((out[first:], got[1], got[2]), want):
+        assert torch.equal(a, b)
